@@ -534,6 +534,101 @@ int fused_moe_down_combine(int32_t dtype, const void* w2, const void* w2_scale,
                            void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Rows of a plan: tokens into the plan's rows and back, and the gradients.
+ *
+ * A caller that runs experts of its own on the plan (training in bf16, other
+ * weight formats) needs the steps around them: the tokens gathered into the
+ * rows of sorted_token_ids, the experts' rows brought back with the routing
+ * weights, and the gradients of both and of the router.  The pages name the
+ * first two as stages of the forward ([hpc-ops RFC] "Background": gather,
+ * top-k weighted reduction); the gradients follow from them.
+ *
+ * Common arguments:
+ *   elem             moe_elem of the rows and tokens.
+ *   T, K             tokens and columns (any K >= 1; a row pitch that is a
+ *                    multiple of 16 bytes is fastest).
+ *   top_k, n_shared  routes per token: top_k routed ones, ids t*top_k + j,
+ *                    then n_shared shared ones, ids T*top_k + t*n_shared + s
+ *                    (moe_align_shared; 0 for moe_align's plans).
+ *   rows_cap         rows of the row buffers and of sorted_token_ids
+ *                    (moe_align_capacity's *sorted_cap).
+ *   sorted_token_ids, num_tokens_post_padded
+ *                    the planner's outputs, read on the device.
+ *   row_of_route     (T * (top_k + n_shared)) int32: moe_route_rows' output
+ *                    for that plan: the row of each route, -1 for a route
+ *                    that has none.  An index outside [0, rows_cap) counts
+ *                    as -1.
+ * Rows at or past num_tokens_post_padded are neither read nor written.
+ * Buffers must not overlap.  Every result is a sum in route order with one
+ * rounding at the end (no atomics): the same inputs give the same bits.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T < 0, K < 1, top_k < 1, n_shared < 0,
+ * rows_cap outside [0, 2^31), T*(top_k + n_shared) >= 2^31),
+ * MOE_ERR_UNSUPPORTED (elem; T * (K / 1024 + 1) or T * (top_k + n_shared),
+ * plus rows_cap / 4, past 2^24), MOE_ERR_ALIGN, MOE_ERR_HIP.
+ */
+typedef enum {
+  MOE_ELEM_BF16 = 0,
+  MOE_ELEM_F16 = 1,
+  MOE_ELEM_F32 = 2,
+  MOE_ELEM_U8 = 3 /* any bytes (e4m3 values, e8m0 scales): moe_permute only */
+} moe_elem;
+
+/* The inverse of the plan: row_of_route[sorted_token_ids[p]] = p, and -1 for
+ * the routes whose expert id is outside [0, E).  topk_ids, top_k, E and
+ * n_shared are those the plan was made from.  T == 0 writes nothing. */
+int moe_route_rows(const int32_t* topk_ids, int64_t T, int32_t top_k, int32_t E, int32_t n_shared,
+                   const int32_t* sorted_token_ids, const int32_t* num_tokens_post_padded,
+                   int64_t rows_cap, int32_t* row_of_route, void* stream);
+
+/* rows[row_of_route[r]] = x[token of r] for every placed route r, and zeros in
+ * the padding rows (sorted_token_ids -1) below num_tokens_post_padded, so that
+ * products over whole blocks, and the weight gradients summed over them, see
+ * nothing there.  x (T, K), rows (rows_cap, K). */
+int moe_permute(int32_t elem, const void* x, const int32_t* row_of_route,
+                const int32_t* sorted_token_ids, const int32_t* num_tokens_post_padded, void* rows,
+                int64_t T, int64_t K, int32_t top_k, int32_t n_shared, int64_t rows_cap,
+                void* stream);
+
+/* Gradient of moe_permute: d_x[t] = the sum of d_rows over t's placed routes,
+ * fp32 (zeros for a token with none).  d_rows (rows_cap, K), d_x (T, K). */
+int moe_permute_backward(int32_t elem, const void* d_rows, const int32_t* row_of_route, void* d_x,
+                         int64_t T, int64_t K, int32_t top_k, int32_t n_shared, int64_t rows_cap,
+                         void* stream);
+
+/* out[t] = the sum over t's placed routes of weight * rows[row_of_route[r]],
+ * fp32: topk_weights[t][j] (T, top_k) for the routed ones (NULL: all 1), 1 for
+ * the shared ones; zeros for a token with no placed route.  A route without a
+ * row adds nothing whatever its weight.  row_of_route NULL: route r's row is
+ * row r.  rows (rows_cap, K), out (T, K). */
+int moe_unpermute(int32_t elem, const void* rows, const int32_t* row_of_route,
+                  const float* topk_weights, void* out, int64_t T, int64_t K, int32_t top_k,
+                  int32_t n_shared, int64_t rows_cap, void* stream);
+
+/* Gradients of moe_unpermute.  d_rows[row_of_route[r]] = weight * d_out[token
+ * of r], zeros in the padding rows below num_tokens_post_padded;
+ * d_weights[t][j] = <rows[row], d_out[t]> in fp32 (0 where the route has no
+ * row).  d_weights NULL: only d_rows (rows is then not read and may be NULL).
+ * topk_weights NULL: all 1.  d_out (T, K), rows and d_rows (rows_cap, K),
+ * d_weights (T, top_k) fp32. */
+int moe_unpermute_backward(int32_t elem, const void* d_out, const void* rows,
+                           const int32_t* row_of_route, const int32_t* sorted_token_ids,
+                           const int32_t* num_tokens_post_padded, const float* topk_weights,
+                           void* d_rows, float* d_weights, int64_t T, int64_t K, int32_t top_k,
+                           int32_t n_shared, int64_t rows_cap, void* stream);
+
+/* Gradient of moe_route_align's weights: topk_ids and topk_weights as it wrote
+ * them, d_weights (T, top_k) fp32 the weights' gradient,
+ *   d_logits[t][e] = sum over j with topk_ids[t][j] = e of
+ *                    w_j (d_weights_j - sum_i w_i d_weights_i),
+ * zeros elsewhere; (T, E) fp32, every element written.  The selection itself
+ * has no gradient.  An id outside [0, E) takes part in the inner sum only.
+ * E <= 1024, top_k <= 16, T < 2^26.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE,
+ * MOE_ERR_UNSUPPORTED, MOE_ERR_ALIGN, MOE_ERR_HIP. */
+int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const float* d_weights,
+                       float* d_logits, int64_t T, int32_t E, int32_t top_k, void* stream);
+
+/*
  * Diagnostic, not a step of the forward: one 128-wide K step of the matrix
  * instruction each dtype's kernels use, D = C + A . B^T, per 16 x 16 tile,
  * through the kernels' own operand layout and instruction wrappers.  The

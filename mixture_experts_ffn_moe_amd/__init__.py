@@ -15,6 +15,8 @@ Entry points (same names as the C ABI):
   fused_moe_fp8_blockwise(x, x_scale, w1, w1_scale, w2, w2_scale, ...)
   fused_moe_mxfp8(x, x_scale, w1, w1_scale, w2, w2_scale, ...)
   fused_moe_mxfp4(x, x_scale, w1, w1_scale, w2, w2_scale, ...)   (packed e2m1 weights)
+  moe_route_rows, moe_permute, moe_unpermute (and _backward), moe_route_backward
+      tokens into the rows of a plan and back, with the gradients
 plus the host helpers moe_align_capacity, moe_workspace_size,
 moe_workspace_layout, moe_ring_layout, moe_select_split and moe_select_block_m.
 ``split=2`` runs the persistent ring mode (block_m 16 or 32).
@@ -35,6 +37,8 @@ __all__ = [
     "moe_route_align", "moe_route_align_workspace_size", "moe_align_shared", "fused_moe_shared",
     "moe_mfma_probe", "moe_align_workspace_size", "MoeTune", "fused_moe_down_combine",
     "fused_moe_fp8_blockwise_noalloc",
+    "moe_route_rows", "moe_permute", "moe_permute_backward", "moe_unpermute",
+    "moe_unpermute_backward", "moe_route_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi355x.so")
@@ -51,6 +55,8 @@ EXPORTED_SYMBOLS = (
     "moe_align_shared", "fused_moe_shared", "moe_ring_layout", "moe_ring_schedule",
     "moe_select_block_m_routed", "moe_align_ws_size", "moe_align_ws", "moe_mfma_probe",
     "moe_align_workspace_size", "fused_moe_down_combine", "fused_moe_fp8_blockwise_noalloc",
+    "moe_route_rows", "moe_permute", "moe_permute_backward", "moe_unpermute",
+    "moe_unpermute_backward", "moe_route_backward",
 )
 
 _STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SHAPE", -3: "MOE_ERR_UNSUPPORTED",
@@ -115,6 +121,13 @@ def lib():
     L.moe_route_align.argtypes = [_P, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]
     L.moe_align_shared.argtypes = [_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P]
     L.fused_moe_shared.argtypes = [_I32, _P, _P, _P, _P, _P, _P, _I32] + tail
+    sizes = [_I64, _I64, _I32, _I32, _I64, _P]
+    L.moe_route_rows.argtypes = [_P, _I64, _I32, _I32, _I32, _P, _P, _I64, _P, _P]
+    L.moe_permute.argtypes = [_I32, _P, _P, _P, _P, _P] + sizes
+    L.moe_permute_backward.argtypes = [_I32, _P, _P, _P] + sizes
+    L.moe_unpermute.argtypes = [_I32, _P, _P, _P, _P] + sizes
+    L.moe_unpermute_backward.argtypes = [_I32, _P, _P, _P, _P, _P, _P, _P, _P] + sizes
+    L.moe_route_backward.argtypes = [_P, _P, _P, _P, _I64, _I32, _I32, _P]
     for name in EXPORTED_SYMBOLS:
         if name != "moe_last_error":
             getattr(L, name).restype = ctypes.c_int
@@ -480,6 +493,192 @@ def fused_moe_down_combine(dtype, w2, w2_scale, sorted_token_ids, expert_ids,
                                         _ptr(workspace),
                                         workspace.numel() * workspace.element_size(),
                                         _stream(stream)))
+    return out
+
+
+# Element types of the row operators (moe_elem of the C ABI); one-byte rows are
+# moved as bytes.
+_ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.uint8: 3, torch.int8: 3,
+         torch.float8_e4m3fn: 3}
+
+
+def _operand(t, name, dtype, shape, dev):
+    """Checks a dense tensor argument of the operators below; returns its address."""
+    if t.dtype is not dtype and t.dtype != dtype:
+        raise MoeError(-3, f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise MoeError(-2, f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.device != dev:
+        raise MoeError(-2, f"{name} must be on {dev} (got {t.device})")
+    if not t.is_contiguous():
+        raise MoeError(-2, f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _elem(t, name):
+    e = _ELEM.get(t.dtype)
+    if e is None:
+        raise MoeError(-3, f"{name}: unsupported type {t.dtype}")
+    _on_gpu(t, name)
+    return e
+
+
+def _on_gpu(t, name):
+    if not t.is_cuda:
+        raise MoeError(-2, f"{name} must be on a GPU (got {t.device})")
+
+
+def _output(out, name, shape, dtype, dev, stream):
+    """The caller's output, checked, or a new one of the stream the call runs on."""
+    if out is not None:
+        _operand(out, name, dtype, shape, dev)
+        return out
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _enqueue(fn, dev, stream, *args):
+    """Calls an entry point on the tensors' device: on its current stream, or on ``stream``."""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        if stream.device != dev:
+            raise MoeError(-2, f"the stream is on {stream.device}, the tensors on {dev}")
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status != 0:
+        raise MoeError(status, lib().moe_last_error().decode())
+
+
+def _routes(n, top_k, n_shared):
+    """Tokens of a plan with n routes."""
+    per = top_k + n_shared
+    if top_k < 1 or n_shared < 0 or n % per:
+        raise MoeError(-2, f"{n} routes are no whole number of tokens with top_k {top_k} and "
+                           f"n_shared {n_shared}")
+    return n // per
+
+
+def moe_route_rows(topk_ids, num_experts, sorted_token_ids, num_tokens_post_padded, n_shared=0,
+                   stream=None, out=None):
+    """The inverse of a plan: (T * (top_k + n_shared)) int32, the row of each
+    route in the plan moe_align / moe_align_shared made of ``topk_ids``, -1
+    for a route that has none.  One such map serves the four calls below."""
+    T, k = topk_ids.shape
+    dev = topk_ids.device
+    _on_gpu(topk_ids, "topk_ids")
+    cap = sorted_token_ids.numel()
+    ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    plan = _operand(sorted_token_ids, "sorted_token_ids", torch.int32, (cap,), dev)
+    ntp = _operand(num_tokens_post_padded, "num_tokens_post_padded", torch.int32, (1,), dev)
+    out = _output(out, "out", (T * (k + n_shared),), torch.int32, dev, stream)
+    _enqueue(lib().moe_route_rows, dev, stream, ids, T, k, num_experts, n_shared, plan, ntp, cap,
+             out.data_ptr())
+    return out
+
+
+def moe_permute(x, row_of_route, sorted_token_ids, num_tokens_post_padded, top_k, n_shared=0,
+                stream=None, out=None):
+    """Tokens (T, K) into the rows of a plan: (len(sorted_token_ids), K), each
+    routed token in its routes' rows, zeros in the padding rows.  Rows at or
+    past num_tokens_post_padded are left as they are (unspecified in a new
+    tensor).  x: bf16, fp16, fp32, or one-byte values (e4m3, scales)."""
+    T, K = x.shape
+    dev = x.device
+    elem = _elem(x, "x")
+    cap = sorted_token_ids.numel()
+    xp = _operand(x, "x", x.dtype, (T, K), dev)
+    row = _operand(row_of_route, "row_of_route", torch.int32, (T * (top_k + n_shared),), dev)
+    plan = _operand(sorted_token_ids, "sorted_token_ids", torch.int32, (cap,), dev)
+    ntp = _operand(num_tokens_post_padded, "num_tokens_post_padded", torch.int32, (1,), dev)
+    out = _output(out, "out", (cap, K), x.dtype, dev, stream)
+    _enqueue(lib().moe_permute, dev, stream, elem, xp, row, plan, ntp, out.data_ptr(), T, K, top_k,
+             n_shared, cap)
+    return out
+
+
+def moe_permute_backward(d_rows, row_of_route, top_k, n_shared=0, stream=None, out=None):
+    """Gradient of moe_permute: each token's sum of its rows' gradients."""
+    cap, K = d_rows.shape
+    dev = d_rows.device
+    elem = _elem(d_rows, "d_rows")
+    n = row_of_route.numel()
+    T = _routes(n, top_k, n_shared)
+    g = _operand(d_rows, "d_rows", d_rows.dtype, (cap, K), dev)
+    row = _operand(row_of_route, "row_of_route", torch.int32, (n,), dev)
+    out = _output(out, "out", (T, K), d_rows.dtype, dev, stream)
+    _enqueue(lib().moe_permute_backward, dev, stream, elem, g, row, out.data_ptr(), T, K, top_k,
+             n_shared, cap)
+    return out
+
+
+def moe_unpermute(rows, row_of_route, topk_weights, top_k, n_shared=0, stream=None, out=None):
+    """The rows of a plan back to their tokens: out[t] = the sum over its
+    routes of topk_weights[t, j] * row (weight 1 for shared routes, and for
+    all of them without ``topk_weights``).  A token without rows gets zeros.
+    ``row_of_route`` None: row r holds route r."""
+    cap, K = rows.shape
+    dev = rows.device
+    elem = _elem(rows, "rows")
+    n = cap if row_of_route is None else row_of_route.numel()
+    T = _routes(n, top_k, n_shared)
+    y = _operand(rows, "rows", rows.dtype, (cap, K), dev)
+    row = None if row_of_route is None else _operand(row_of_route, "row_of_route", torch.int32,
+                                                     (n,), dev)
+    w = None if topk_weights is None else _operand(topk_weights, "topk_weights", torch.float32,
+                                                   (T, top_k), dev)
+    out = _output(out, "out", (T, K), rows.dtype, dev, stream)
+    _enqueue(lib().moe_unpermute, dev, stream, elem, y, row, w, out.data_ptr(), T, K, top_k,
+             n_shared, cap)
+    return out
+
+
+def moe_unpermute_backward(d_out, rows, row_of_route, sorted_token_ids, num_tokens_post_padded,
+                           topk_weights, top_k, n_shared=0, stream=None, out=None):
+    """Gradients of moe_unpermute: (d_rows, d_weights), the rows' in the
+    plan's order with zeros in its padding rows (rows at or past
+    num_tokens_post_padded are left as they are), the weights' (T, top_k)
+    fp32.  ``rows`` None: only d_rows, and d_weights is None.  ``out`` may pass
+    the two preallocated."""
+    T, K = d_out.shape
+    dev = d_out.device
+    elem = _elem(d_out, "d_out")
+    cap = sorted_token_ids.numel()
+    g = _operand(d_out, "d_out", d_out.dtype, (T, K), dev)
+    y = None if rows is None else _operand(rows, "rows", d_out.dtype, (cap, K), dev)
+    row = _operand(row_of_route, "row_of_route", torch.int32, (T * (top_k + n_shared),), dev)
+    plan = _operand(sorted_token_ids, "sorted_token_ids", torch.int32, (cap,), dev)
+    ntp = _operand(num_tokens_post_padded, "num_tokens_post_padded", torch.int32, (1,), dev)
+    w = None if topk_weights is None else _operand(topk_weights, "topk_weights", torch.float32,
+                                                   (T, top_k), dev)
+    d_rows, d_w = (None, None) if out is None else out
+    d_rows = _output(d_rows, "d_rows", (cap, K), d_out.dtype, dev, stream)
+    d_w = None if rows is None else _output(d_w, "d_weights", (T, top_k), torch.float32, dev,
+                                            stream)
+    _enqueue(lib().moe_unpermute_backward, dev, stream, elem, g, y, row, plan, ntp, w,
+             d_rows.data_ptr(), None if d_w is None else d_w.data_ptr(), T, K, top_k, n_shared,
+             cap)
+    return d_rows, d_w
+
+
+def moe_route_backward(topk_ids, topk_weights, d_weights, num_experts, stream=None, out=None):
+    """Gradient of moe_route_align's weights with respect to its logits,
+    (T, num_experts) fp32, from topk_ids and topk_weights as it returned them
+    and the weights' gradient."""
+    T, k = topk_ids.shape
+    dev = topk_ids.device
+    _on_gpu(topk_ids, "topk_ids")
+    ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    w = _operand(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+    d = _operand(d_weights, "d_weights", torch.float32, (T, k), dev)
+    out = _output(out, "out", (T, num_experts), torch.float32, dev, stream)
+    _enqueue(lib().moe_route_backward, dev, stream, ids, w, d, out.data_ptr(), T, num_experts, k)
     return out
 
 

@@ -9,6 +9,7 @@
 #include "../../include/moe.h"
 #include "device.h"
 #include "launch.h"
+#include "ops.h"
 
 namespace {
 
@@ -376,6 +377,16 @@ int scratch_for_current_device(void** out) {
 }
 
 }  // namespace
+
+int abi_fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+int abi_ok() { return ok(); }
 
 extern "C" {
 

@@ -1,0 +1,41 @@
+// ops.h -- internal launchers of the operators around the plan (rows.hip) and
+// of the 4-bit products (w4.hip), and the error reporting they share with
+// abi.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+// Records the message of a failing call and returns `code` / clears the
+// message and returns MOE_OK (the calling thread's, as moe_last_error reads it).
+int abi_fail(int code, const char* fmt, ...);
+int abi_ok();
+
+// Element types, in the order of moe_elem.
+enum : int { ELEM_BF16 = 0, ELEM_F16 = 1, ELEM_F32 = 2, ELEM_U8 = 3 };
+constexpr int elem_bytes(int elem) { return elem == ELEM_F32 ? 4 : elem == ELEM_U8 ? 1 : 2; }
+
+// Routes of a plan: T tokens with top_k routed and n_shared shared routes
+// each; route ids t * top_k + j, then T * top_k + t * n_shared + s.
+struct RowsArgs {
+  const int32_t* sorted;  // plan: route id of each row, -1 for padding
+  const int32_t* ntp;     // rows in use (device scalar)
+  const int32_t* row;     // row of each route, -1 where it has none (null: row r is route r)
+  const float* w;         // (T, top_k) weights, or null for ones
+  int64_t T, K, cap;      // tokens, columns, rows of the buffers
+  int top_k, n_shared;
+};
+
+hipError_t launch_route_rows(const int32_t* ids, const RowsArgs& a, int E, int32_t* row,
+                             hipStream_t stream);
+hipError_t launch_permute(int elem, const RowsArgs& a, const void* x, void* rows,
+                          hipStream_t stream);
+hipError_t launch_unpermute(int elem, const RowsArgs& a, const void* rows, void* out,
+                            hipStream_t stream);
+hipError_t launch_unpermute_backward(int elem, const RowsArgs& a, const void* d_out,
+                                     const void* rows, void* d_rows, float* d_w,
+                                     hipStream_t stream);
+hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw,
+                                 float* d_logits, int64_t T, int E, int top_k,
+                                 hipStream_t stream);

@@ -16,6 +16,8 @@ moe      the expert FFN step by step in fp64: dequantize, gate/up GEMM,
          SwiGLU, requantize, down GEMM, top-k weighted sum.
 router   the gate's routing from router logits: softmax over the experts,
          the top-k largest (ties to the lower id), renormalized weights.
+rows     tokens into the rows of a plan and back, their gradients and the
+         router's.
 
 Every function cites the page and passage of the source pages it follows.
 The sources are five web pages on fused MoE kernels:
