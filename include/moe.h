@@ -629,6 +629,62 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const
                        float* d_logits, int64_t T, int32_t E, int32_t top_k, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Weight-only 4-bit products for a few tokens.
+ *
+ * fused_moe_mxfp4 quantizes the activations to MX FP8 and works on blocks of
+ * a plan; these calls keep bf16 or fp16 activations, take the routing as it
+ * is (no planner) and serve decode steps, where the weights' bytes are the
+ * time.
+ *
+ * Common arguments:
+ *   format           MOE_W4_INT: W = (q - z) * s, q whole in 0..15, scales s
+ *                    of the activations' type (E, N, K/group), zero points z
+ *                    uint8 0..15 of the same shape or NULL (z = 8);
+ *                    MOE_W4_MX: e2m1 codes times e8m0 scales per 32 (uint8,
+ *                    as fused_moe_mxfp4's weights; 255 is NaN), no zeros.
+ *                    Both pack two codes a byte along the contraction,
+ *                    element 2j in the low nibble of byte j.
+ *   elem             MOE_ELEM_BF16 or MOE_ELEM_F16: x, out and int4 scales.
+ *   group            elements of a scale group along the contraction: 32, 64
+ *                    or 128, or 0 for one group per row; MOE_W4_MX: 32.  The
+ *                    contraction is a multiple of it (of 128 for 0).
+ *   topk_ids         (T, top_k) int32: expert of each route.  A route whose
+ *                    id is outside [0, E) gives zeros.
+ * Limits: T * top_k <= 4096 routes, N * K < 2^32.  An expert's weights are
+ * read once for up to 16 of its routes (bf16; 8 for fp16 and in the second
+ * product of fused_moe_w4).  Sums are fp32 in a fixed order: the same inputs
+ * give the same bits.  An infinite activation gives NaN.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_ALIGN,
+ * MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 is a successful no-op.
+ */
+typedef enum { MOE_W4_INT = 0, MOE_W4_MX = 1 } moe_w4_format;
+
+/* out[r] = W[topk_ids[r]] . x, rounded once to elem: x (T, K) for every route
+ * of a token, or with x_per_route (T, top_k, K); w (E, N, K/2) bytes; out (T,
+ * top_k, N).  With swiglu rows [0, N/2) are the gate and [N/2, N) the up
+ * projection, and out (T, top_k, N/2) = silu(gate) * up.  topk_ids NULL: one
+ * expert (E = top_k = 1), a plain linear layer such as a shared expert's. */
+int moe_w4_matvec(int32_t format, int32_t elem, const void* x, int32_t x_per_route, const void* w,
+                  const void* w_scale, const uint8_t* w_zero, const int32_t* topk_ids, void* out,
+                  int64_t T, int64_t K, int64_t N, int32_t E, int32_t top_k, int32_t group,
+                  int32_t swiglu, void* stream);
+
+/* The whole expert FFN: out[t] = sum_j topk_weights[t][j] * W2[e] . silu(gate)
+ * * up, with gate, up = W1[e] . x[t], for the routes with e = topk_ids[t][j]
+ * in [0, E); one rounding to elem at the end, the intermediate held in fp32
+ * (and entering the second product as two bf16 parts).  w1 (E, N, K/2), w2
+ * (E, K, N/4) bytes, N = 2I, with scales and zeros along K and I.  The
+ * workspace (device, 16-byte aligned, contents undefined on return; separate
+ * for calls that may overlap) has at least moe_w4_workspace_size bytes. */
+int moe_w4_workspace_size(int64_t T, int64_t K, int64_t N, int32_t top_k, size_t* bytes);
+int fused_moe_w4(int32_t format, int32_t elem, const void* x, const void* w1, const void* w1_scale,
+                 const uint8_t* w1_zero, const void* w2, const void* w2_scale,
+                 const uint8_t* w2_zero, const int32_t* topk_ids, const float* topk_weights,
+                 void* out, int64_t T, int64_t K, int64_t N, int32_t E, int32_t top_k,
+                 int32_t group, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Diagnostic, not a step of the forward: one 128-wide K step of the matrix
  * instruction each dtype's kernels use, D = C + A . B^T, per 16 x 16 tile,
  * through the kernels' own operand layout and instruction wrappers.  The

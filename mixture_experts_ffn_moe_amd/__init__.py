@@ -17,6 +17,8 @@ Entry points (same names as the C ABI):
   fused_moe_mxfp4(x, x_scale, w1, w1_scale, w2, w2_scale, ...)   (packed e2m1 weights)
   moe_route_rows, moe_permute, moe_unpermute (and _backward), moe_route_backward
       tokens into the rows of a plan and back, with the gradients
+  moe_w4_matvec, fused_moe_w4
+      products with 4-bit weights for a few tokens, alone and as the experts' FFN
 plus the host helpers moe_align_capacity, moe_workspace_size,
 moe_workspace_layout, moe_ring_layout, moe_select_split and moe_select_block_m.
 ``split=2`` runs the persistent ring mode (block_m 16 or 32).
@@ -39,6 +41,7 @@ __all__ = [
     "fused_moe_fp8_blockwise_noalloc",
     "moe_route_rows", "moe_permute", "moe_permute_backward", "moe_unpermute",
     "moe_unpermute_backward", "moe_route_backward",
+    "moe_w4_matvec", "moe_w4_workspace_size", "fused_moe_w4",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi355x.so")
@@ -57,6 +60,7 @@ EXPORTED_SYMBOLS = (
     "moe_align_workspace_size", "fused_moe_down_combine", "fused_moe_fp8_blockwise_noalloc",
     "moe_route_rows", "moe_permute", "moe_permute_backward", "moe_unpermute",
     "moe_unpermute_backward", "moe_route_backward",
+    "moe_w4_matvec", "moe_w4_workspace_size", "fused_moe_w4",
 )
 
 _STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SHAPE", -3: "MOE_ERR_UNSUPPORTED",
@@ -128,6 +132,11 @@ def lib():
     L.moe_unpermute.argtypes = [_I32, _P, _P, _P, _P] + sizes
     L.moe_unpermute_backward.argtypes = [_I32, _P, _P, _P, _P, _P, _P, _P, _P] + sizes
     L.moe_route_backward.argtypes = [_P, _P, _P, _P, _I64, _I32, _I32, _P]
+    L.moe_w4_matvec.argtypes = [_I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32,
+                                _I32, _I32, _I32, _P]
+    L.moe_w4_workspace_size.argtypes = [_I64, _I64, _I64, _I32, ctypes.POINTER(_SZ)]
+    L.fused_moe_w4.argtypes = [_I32, _I32] + [_P] * 10 + [_I64, _I64, _I64, _I32, _I32, _I32, _P,
+                                                          _SZ, _P]
     for name in EXPORTED_SYMBOLS:
         if name != "moe_last_error":
             getattr(L, name).restype = ctypes.c_int
@@ -679,6 +688,102 @@ def moe_route_backward(topk_ids, topk_weights, d_weights, num_experts, stream=No
     d = _operand(d_weights, "d_weights", torch.float32, (T, k), dev)
     out = _output(out, "out", (T, num_experts), torch.float32, dev, stream)
     _enqueue(lib().moe_route_backward, dev, stream, ids, w, d, out.data_ptr(), T, num_experts, k)
+    return out
+
+
+# Formats of 4-bit weights (moe_w4_format of the C ABI).
+_W4_FORMAT = {"int4": 0, "mx": 1}
+
+
+def _w4_weights(fmt, name, w, scale, zero, E, N, K, group, elem_type, dev):
+    """Checks one set of 4-bit weights; returns the three addresses."""
+    n = K // group if group else 1
+    wp = _operand(w, name, torch.uint8, (E, N, K // 2), dev)
+    sp = _operand(scale, name + "_scale", torch.uint8 if fmt else elem_type, (E, N, n), dev)
+    zp = None if zero is None else _operand(zero, name + "_zero", torch.uint8, (E, N, n), dev)
+    return wp, sp, zp
+
+
+def _w4_types(fmt, x):
+    f = _W4_FORMAT.get(fmt)
+    if f is None:
+        raise MoeError(-3, f"unknown 4-bit format {fmt!r}: 'int4' or 'mx'")
+    elem = _elem(x, "x")
+    if elem > 1:
+        raise MoeError(-3, f"x must be bf16 or fp16 (got {x.dtype})")
+    return f, elem
+
+
+def moe_w4_matvec(fmt, x, w, w_scale, w_zero, topk_ids, group, swiglu=False, stream=None,
+                  out=None):
+    """Products of a few tokens with 4-bit weights, one per route.
+
+    fmt "int4": codes q in 0..15, (q - zero) * scale with the scales of x's
+    type per ``group`` (32, 64, 128; 0 for one per row) and uint8 ``w_zero``
+    or None (8); "mx": e2m1 codes and uint8 e8m0 scales per 32.  w (E, N, K/2)
+    uint8, element 2j in the low nibble of byte j.  x (T, K), or (T, top_k, K)
+    for one vector a route.  Returns (T, top_k, N), or (T, top_k, N/2) =
+    silu(gate) * up with ``swiglu``; zeros for a route whose expert is outside
+    [0, E).  ``topk_ids`` None: one expert, (T, K) -> (T, N).  At most 4,096
+    routes."""
+    f, elem = _w4_types(fmt, x)
+    dev = x.device
+    if w.dim() != 3:
+        raise MoeError(-2, f"w must have shape (E, N, K/2) (got {tuple(w.shape)})")
+    E, N, _ = w.shape
+    T, K = x.shape[0], x.shape[-1]
+    n = N // 2 if swiglu else N
+    if topk_ids is None:
+        k, ids, per_route = 1, None, 0
+        xp = _operand(x, "x", x.dtype, (T, K), dev)
+        shape = (T, n)
+    else:
+        k = topk_ids.shape[1]
+        per_route = int(x.dim() == 3)
+        xp = _operand(x, "x", x.dtype, (T, k, K) if per_route else (T, K), dev)
+        ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+        shape = (T, k, n)
+    wp, sp, zp = _w4_weights(f, "w", w, w_scale, w_zero, E, N, K, group, x.dtype, dev)
+    out = _output(out, "out", shape, x.dtype, dev, stream)
+    _enqueue(lib().moe_w4_matvec, dev, stream, f, elem, xp, per_route, wp, sp, zp, ids,
+             out.data_ptr(), T, K, N, E, k, group, int(swiglu))
+    return out
+
+
+def moe_w4_workspace_size(T, K, N, top_k):
+    """Workspace bytes of fused_moe_w4 (N = 2I, the gate and up rows)."""
+    out = _SZ()
+    _check(lib().moe_w4_workspace_size(T, K, N, top_k, ctypes.byref(out)))
+    return out.value
+
+
+def fused_moe_w4(fmt, x, w1, w1_scale, w1_zero, w2, w2_scale, w2_zero, topk_ids, topk_weights,
+                 group, out=None, workspace=None, stream=None):
+    """The experts' FFN of a few tokens with 4-bit weights, from the routing to
+    the weighted sum (no planner): formats as moe_w4_matvec, w1 (E, 2I, K/2)
+    with the gate rows first, w2 (E, K, I/2).  Shared experts are more experts
+    that every token routes to with weight 1."""
+    f, elem = _w4_types(fmt, x)
+    dev = x.device
+    if w1.dim() != 3 or x.dim() != 2 or topk_ids.dim() != 2:
+        raise MoeError(-2, "x must be (T, K), w1 (E, N, K/2) and topk_ids (T, top_k)")
+    E, N, _ = w1.shape
+    T, K = x.shape
+    k = topk_ids.shape[1]
+    xp = _operand(x, "x", x.dtype, (T, K), dev)
+    p1 = _w4_weights(f, "w1", w1, w1_scale, w1_zero, E, N, K, group, x.dtype, dev)
+    p2 = _w4_weights(f, "w2", w2, w2_scale, w2_zero, E, K, N // 2, group, x.dtype, dev)
+    ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    wt = _operand(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+    out = _output(out, "out", (T, K), x.dtype, dev, stream)
+    if workspace is None:
+        workspace = _output(None, "workspace", (moe_w4_workspace_size(T, K, N, k),), torch.uint8,
+                            dev, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise MoeError(-2, f"workspace must be a contiguous tensor on {dev}")
+    _enqueue(lib().fused_moe_w4, dev, stream, f, elem, xp, *p1, *p2, ids, wt, out.data_ptr(), T, K,
+             N, E, k, group, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size())
     return out
 
 

@@ -39,3 +39,25 @@ hipError_t launch_unpermute_backward(int elem, const RowsArgs& a, const void* d_
 hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw,
                                  float* d_logits, int64_t T, int E, int top_k,
                                  hipStream_t stream);
+
+// 4-bit weights: formats in the order of moe_w4_format.
+enum : int { W4_INT = 0, W4_MX = 1 };
+
+// One set of products y[r] = W[e(r)] x[r or its token] with 4-bit weights.
+struct W4Args {
+  const void* x;       // (T, K), or (R, K) with x_per_route; xelem
+  const uint8_t* w;    // (E, N, K / 2)
+  const void* scale;   // (E, N, K / group): scale_elem, or e8m0
+  const uint8_t* zero; // (E, N, K / group), or null for 8
+  const int32_t* ids;  // (R) expert of each route; null: one expert, every route
+  void* out;           // (R, N), or (R, N / 2) with swiglu; oelem
+  int K, N, E, R, top_k, group;
+  int xelem, oelem, scale_elem;
+  int x_per_route, swiglu;
+};
+
+constexpr int kW4MaxRoutes = 4096;  // routes of one call (a workgroup lists its expert's)
+hipError_t launch_w4(int format, const W4Args& a, hipStream_t stream);
+// out[t] = sum over t's routes with an expert in [0, E) of w[r] y[r]; y (R, K) fp32
+hipError_t launch_w4_combine(const float* y, const int32_t* ids, const float* w, void* out,
+                             int oelem, int T, int top_k, int K, int E, hipStream_t stream);

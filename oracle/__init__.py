@@ -16,6 +16,7 @@ moe      the expert FFN step by step in fp64: dequantize, gate/up GEMM,
          SwiGLU, requantize, down GEMM, top-k weighted sum.
 router   the gate's routing from router logits: softmax over the experts,
          the top-k largest (ties to the lower id), renormalized weights.
+w4       products with 4-bit weights, and the FFN of a few tokens.
 rows     tokens into the rows of a plan and back, their gradients and the
          router's.
 
