@@ -54,6 +54,7 @@ struct W4Args {
   int K, N, E, R, top_k, group;
   int xelem, oelem, scale_elem;
   int x_per_route, swiglu;
+  uint32_t inv_top_k;  // ceil(2^32 / top_k): r / top_k = umulhi(r, inv) for r < 4096 (top_k > 1)
 };
 
 constexpr int kW4MaxRoutes = 4096;  // routes of one call (a workgroup lists its expert's)

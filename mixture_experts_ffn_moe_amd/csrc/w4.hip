@@ -27,20 +27,27 @@
 // of 32 and 64 need the elements of one instruction to lie in one group: the
 // four dwords of the four lane groups are transposed by lane-row swaps.
 //
-// A workgroup has 8 waves on the same 16 or 32 weight rows; wave w takes the
-// steps w, w + 8, ... of K, and the waves' sums are added through LDS at the
-// end.  The tokens' part of K lies in LDS, in the order the weights need.
+// A workgroup has 4 waves on the same 16 or 32 weight rows; each takes a run of
+// steps of K, D of them requested ahead with one load for the D steps' scales
+// (a load of one step's touches 16 rows' lines for two bytes each, and costs the
+// address unit as much as the weights'), and the waves' sums are added through
+// LDS at the end.  The tokens' part of K lies in LDS, in the order
+// the weights need.  Where there are many tiles a workgroup takes several in a
+// row, requesting the next one's weights while it ends the last.
 #include "device.h"
 #include "ops.h"
 
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 constexpr int kTile = 16;               // tokens of one pass over the weights
 constexpr int kUnit = kWaves * 128;     // K elements of one step of every wave
 constexpr int kPad = 8;                 // elements behind each token's row in LDS
-constexpr int kDepth = 4;               // steps a wave requests ahead
+constexpr int kBlocks = 4;              // 64-route blocks found without a barrier
+// LDS of the tokens: a few tokens' whole K, or 1,024 elements of kTile tokens
+// (half as many of two parts).
+constexpr int kTokenLds = kTile * (2 * kUnit + kPad) * 2;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -89,29 +96,31 @@ __device__ __forceinline__ void transpose4(uint4& c) {
   c = make_uint4(e[0], e[1], f[0], f[1]);
 }
 
-// bf16 bits of 8 consecutive activations: part 0 the nearest bf16, part 1 what is left.
+// 8 consecutive activations of a lane: one 16-byte load, or two of fp32.
 template <int XE>
-__device__ __forceinline__ void split8(const uint8_t* p, uint32_t (&b)[parts<XE>()][8]) {
+struct X8 {
+  uint4 v[XE == ELEM_F32 ? 2 : 1];
+};
+
+// Their bf16 bits: part 0 the nearest bf16, part 1 what is left.
+template <int XE>
+__device__ __forceinline__ void split8(const X8<XE>& x, uint32_t (&b)[parts<XE>()][8]) {
+  const uint32_t d[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w};
   if constexpr (XE == ELEM_BF16) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[0][2 * i] = d[i] & 0xFFFFu, b[0][2 * i + 1] = d[i] >> 16;
   } else {
     float f[8];
     if constexpr (XE == ELEM_F16) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      const uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f[2 * i] = bits_to_f32(d[i] & 0xFFFFu, ELEM_F16);
         f[2 * i + 1] = bits_to_f32(d[i] >> 16, ELEM_F16);
       }
     } else {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      const float4 u = *reinterpret_cast<const float4*>(p + 16);
-      f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-      f[4] = u.x, f[5] = u.y, f[6] = u.z, f[7] = u.w;
+      const uint32_t u[4] = {x.v[1].x, x.v[1].y, x.v[1].z, x.v[1].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(d[i]), f[4 + i] = __uint_as_float(u[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -127,29 +136,73 @@ __device__ __forceinline__ void store_out(void* out, size_t at, float v, int ele
   else static_cast<uint16_t*>(out)[at] = f32_to_bf16(v);
 }
 
-// GM: scale groups in a 128-wide step (int4: 1, 2, 4).  NT: 16-row weight
-// tiles of a workgroup; with SWIGLU the gate's and the up's.
-// Grid: x the output tile; y the route whose expert to take (R <= E; only the
-// expert's first route works), the expert (R > E; y = E: the routes without an
-// expert here), or the block of `tile` tokens (no ids).
-template <int FMT, int XE, int GM, int NT, bool SWIGLU>
-__global__ void __launch_bounds__(kThreads)
-k_w4(W4Args a, int tile, int x_bytes) {
+// BYTES consecutive bytes of a table, as dwords.  RAG: at any address, from the
+// dwords that cover them (a dword with a byte of the table in it can be read
+// whole; one behind the buffer's end reads 0).
+template <int BYTES, bool RAG>
+struct Window {
+  static constexpr int N = (BYTES + 3) / 4;
+  uint32_t d[N + RAG];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int off, int soff) {
+    const int at = RAG ? off & ~3 : off;
+    constexpr int M = N + RAG;
+    int i = 0;
+#pragma unroll
+    for (; i + 4 <= M; i += 4) {
+      const uint4 v = buf_load16(r, (uint32_t)at + 4 * i, soff);
+      d[i] = v.x, d[i + 1] = v.y, d[i + 2] = v.z, d[i + 3] = v.w;
+    }
+    if constexpr (M % 4 >= 2) {
+      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, at + 4 * (M / 4 * 4), soff, 0);
+      d[M / 4 * 4] = v[0], d[M / 4 * 4 + 1] = v[1];
+    }
+    if constexpr (M % 2 == 1) d[M - 1] = __builtin_amdgcn_raw_buffer_load_b32(r, at + 4 * (M - 1), soff, 0);
+  }
+  __device__ __forceinline__ void align(int off) {
+    if constexpr (RAG) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) d[i] = __builtin_amdgcn_alignbyte(d[i + 1], d[i], off & 3);
+    }
+  }
+  __device__ __forceinline__ uint32_t u16(int i) const { return d[i / 2] >> (16 * (i % 2)) & 0xFFFFu; }
+  __device__ __forceinline__ uint32_t u8(int i) const { return d[i / 4] >> (8 * (i % 4)) & 0xFFu; }
+};
+
+// A buffer over `bytes` bytes from any address: its base is the dword that holds
+// the first, `skip` bytes further.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t dword_rsrc(const uint8_t* p, uint32_t bytes,
+                                                             int& skip) {
+  skip = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+  return make_rsrc(p - skip, bytes ? (bytes + skip + 3) & ~3u : 0);
+}
+
+// GM: scale groups in a 128-wide step (int4: 1, 2, 4).  RAG: K is no multiple of
+// 512 or a row has one scale, so that the scales of D steps lie at any address,
+// and a row may end inside a step.  NT: 16-row weight tiles taken together; with SWIGLU the
+// gate's and the up's.  D: steps a wave requests ahead.
+// Grid: x the first of `run` output tiles; y the route whose expert to take (R
+// <= E; only the expert's first route works), the expert (R > E; y = E: the
+// routes without an expert here), or the block of `tile` tokens (no ids).
+template <int FMT, int XE, int GM, bool RAG, int NT, bool SWIGLU, int D>
+__global__ void __launch_bounds__(kThreads, GM > 1 ? 2 : NT == 2 && D == 4 && (RAG || XE != ELEM_BF16) ? 3 : 4)
+k_w4(W4Args a, int tile, int run) {
   constexpr int P = parts<XE>();
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* xs = reinterpret_cast<uint16_t*>(smem);
-  float* red = reinterpret_cast<float*>(smem);  // after the tokens' last use
-  uint16_t* list = reinterpret_cast<uint16_t*>(smem + x_bytes);
+  float* red = reinterpret_cast<float*>(smem + kTokenLds);  // waves 1.. of each tile
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + kTokenLds + (kWaves - 1) * NT * 1024);
   __shared__ int wave_count[kWaves];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int n16 = lane & 15, g = lane >> 4;
   const int out_n = SWIGLU ? a.N / 2 : a.N;
   constexpr int kCols = SWIGLU ? 16 : 16 * NT;
-  const int col0 = blockIdx.x * kCols;
+  const int tiles = (out_n + kCols - 1) / kCols;
+  const int tile0 = blockIdx.x * run, tile1 = min(tiles, tile0 + run);
 
   // the workgroup's expert and the routes it works on
-  int e = 0, count, first = 0;
+  int e = 0, count, first = 0, lead = -1;  // lead: the first of them
+  const bool few = a.ids && a.R <= 64 * kBlocks;  // found by every wave alone
   if (!a.ids) {
     first = blockIdx.y * tile;
     count = min(tile, a.R - first);
@@ -158,211 +211,343 @@ k_w4(W4Args a, int tile, int x_bytes) {
     e = a.R <= a.E ? a.ids[y] : y < a.E ? y : -1;
     if ((unsigned)e >= (unsigned)a.E) e = -1;
     count = 0;
-    for (int base = 0; base < a.R; base += kThreads) {
-      const int r = base + tid;
-      int id = -2;
-      if (r < a.R) {
-        id = a.ids[r];
-        if ((unsigned)id >= (unsigned)a.E) id = -1;
+    if (few) {
+      int id[kBlocks];
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) id[b] = a.ids[min(64 * b + lane, a.R - 1)];
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        const bool valid = (unsigned)id[b] < (unsigned)a.E;
+        const unsigned long long m =
+            __ballot(64 * b + lane < a.R && (valid ? id[b] : -1) == e);
+        if (lead < 0 && m) lead = 64 * b + __ffsll(m) - 1;
+        if (wave == 0 && (m >> lane & 1))
+          list[count + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(64 * b + lane);
+        count += __popcll(m);
       }
-      const unsigned long long m = __ballot(id == e);
-      if (lane == 0) wave_count[wave] = __popcll(m);
-      __syncthreads();
-      int at = count;
-      for (int v = 0; v < kWaves; ++v) {
-        if (v < wave) at += wave_count[v];
-        count += wave_count[v];
+    } else {
+      for (int base = 0; base < a.R; base += kThreads) {
+        int id = -2;
+        if (base + tid < a.R) {
+          id = a.ids[base + tid];
+          if ((unsigned)id >= (unsigned)a.E) id = -1;
+        }
+        const unsigned long long m = __ballot(id == e);
+        if (lane == 0) wave_count[wave] = __popcll(m);
+        __syncthreads();
+        int at = count;
+        for (int v = 0; v < kWaves; ++v) {
+          if (v < wave) at += wave_count[v];
+          count += wave_count[v];
+        }
+        if (id == e) list[at + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(base + tid);
+        __syncthreads();
       }
-      if (id == e) list[at + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)r;
-      __syncthreads();
+      if (count) lead = list[0];
     }
-    if (count == 0 || (a.R <= a.E && list[0] != y)) return;
+    if (count == 0 || (a.R <= a.E && lead != y)) return;
     if (e < 0) {  // routes without an expert here: zeros
-      for (int i = tid; i < count * kCols; i += kThreads) {
-        const int c = col0 + i % kCols;
-        if (c < out_n) store_out(a.out, (size_t)list[i / kCols] * out_n + c, 0.f, a.oelem);
-      }
+      if (few) __syncthreads();
+      const int c0 = tile0 * kCols, w = min(out_n, tile1 * kCols) - c0;
+      for (int i = tid; i < count * w; i += kThreads)
+        store_out(a.out, (size_t)list[i / w] * out_n + c0 + i % w, 0.f, a.oelem);
       return;
     }
   }
+  // the m-th of them, m wave-uniform
+  if (few && count > 1) __syncthreads();
+  auto route = [&](int m) -> int {
+    if (!a.ids) return first + m;
+    return count == 1 ? lead : __builtin_amdgcn_readfirstlane((int)list[m]);
+  };
 
   const int KS = (a.K + 127) / 128, KG = a.K / a.group;
+  const int J = (KS + kWaves - 1) / kWaves, JP = (J + D - 1) / D * D;  // steps of a wave
   const uint32_t pitch = (uint32_t)a.K / 2;
   const __amdgpu_buffer_rsrc_t rw =
       make_rsrc(a.w + (size_t)e * a.N * pitch, (uint32_t)a.N * pitch);
-  constexpr int SB = FMT == W4_MX ? 1 : 2;  // bytes of a scale
+  constexpr int SB = FMT == W4_MX ? 1 : 2;       // bytes of a scale
+  constexpr int SG = FMT == W4_MX ? 4 : GM;      // scales of a row in a step
+  int skip_s, skip_z;
   const __amdgpu_buffer_rsrc_t rs =
-      make_rsrc(static_cast<const uint8_t*>(a.scale) + (size_t)e * a.N * KG * SB,
-                (uint32_t)a.N * KG * SB);
+      dword_rsrc(static_cast<const uint8_t*>(a.scale) + (size_t)e * a.N * KG * SB,
+                 (uint32_t)a.N * KG * SB, skip_s);
   const bool has_zero = FMT == W4_INT && a.zero;
-  const __amdgpu_buffer_rsrc_t rz =
-      make_rsrc(has_zero ? a.zero + (size_t)e * a.N * KG : a.w, (uint32_t)a.N * KG);
-  uint32_t wrow[NT], srow[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    int n = SWIGLU ? t * out_n + min(col0 + n16, out_n - 1) : min(col0 + 16 * t + n16, a.N - 1);
-    wrow[t] = (uint32_t)n * pitch + 16 * g;
-    srow[t] = (uint32_t)n * KG;
-  }
-  constexpr uint32_t kNone = 0xFFFFFFF0u;  // past every buffer: the load returns 0
+  const __amdgpu_buffer_rsrc_t rz = dword_rsrc(has_zero ? a.zero + (size_t)e * a.N * KG : a.w,
+                                               has_zero ? (uint32_t)a.N * KG : 0, skip_z);
+  const float z0 = has_zero ? 128.f : 136.f;  // an empty buffer's loads read 0
+  const bool one_scale = GM == 1 && FMT == W4_INT && KG == 1;  // of the whole row
 
   for (int m0 = 0; m0 < count; m0 += tile) {
     const int nt = min(tile, count - m0);
-    // as much of K at a time as the LDS holds for these tokens
-    int kc = (x_bytes / (P * nt * 2) - kPad) / kUnit * kUnit;
-    kc = min(kc, (a.K + kUnit - 1) / kUnit * kUnit);
-    const int xrow = kc + kPad;
+    // steps of each wave in one part of K: what the LDS holds for nt tokens
+    const int fit = (kTokenLds / (P * nt * 2) - kPad) / kUnit;
+    const bool whole = D > 2 || fit >= JP;  // many steps ahead only where K fits
+    const int S = whole ? JP : fit / D * D;  // fit >= D: the launch sees to it
+    const int xrow = S * kUnit + kPad, inv_s = 65536 / S + 1;  // seg * inv_s >> 16 = seg / S
     const uint16_t* xa = xs + (size_t)(n16 < nt ? n16 : 0) * xrow;
-    f32x4 acc[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (int k0 = 0; k0 < a.K; k0 += kc) {
-      const int S = kc / kUnit;  // steps of each wave in this part of K
-      uint4 wq[kDepth][NT];
-      uint32_t sq[kDepth][NT][GM], zq[kDepth][NT][GM];
-      auto request = [&](int slot, int i) {
-        const int step = (k0 / 128) + i * kWaves + wave;
-        if (step >= KS) return;
+    // Requests run D steps ahead of the products (the scales of a round of D
+    // steps a round ahead of its weights), over the parts of K and the tiles in
+    // order.  All are unconditional, so that the waits count them exactly: past
+    // the last tile the rows lie outside the buffers (the loads return zeros and
+    // touch no memory), past the last step the last one is read again.
+    constexpr int kNone = (int)0x80000000;  // past every buffer
+    uint4 wq[D][NT];
+    Window<D * SG * SB, RAG> sn[NT], sc[NT];      // the next round's scales, this one's
+    constexpr bool ZRAG = RAG || D * GM % 4;      // two zero points are no whole dword
+    Window<D * GM, ZRAG> zn[NT], zc[NT];
+    int wrow[NT], srow[NT], zrow[NT];
+    auto weight_row = [&](int t0, int t) {
+      return SWIGLU ? t * out_n + min(t0 * 16 + n16, out_n - 1)
+                    : min((t0 * NT + t) * 16 + n16, a.N - 1);
+    };
+    // a position in the walk: tile, part of K, round's first step in the part
+    struct Pos {
+      int tile, part, i;
+    };
+    Pos pw{tile0, 0, 0}, ps{tile0, 0, 0};
+    auto next_round = [&](Pos& p) {
+      p.i += D;
+      if (p.i < S) return false;
+      p.i = 0;
+      p.part += S * kWaves;
+      if (p.part < KS) return false;
+      p.part = 0;
+      ++p.tile;
+      return true;
+    };
+    auto weight_rows = [&] {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        wrow[t] = pw.tile < tile1 ? (int)((uint32_t)weight_row(pw.tile, t) * pitch + 16 * g) : kNone;
+    };
+    auto scale_rows = [&] {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int n = weight_row(ps.tile, t) * KG;
+        srow[t] = ps.tile < tile1 ? n * SB + skip_s : kNone;
+        zrow[t] = ps.tile < tile1 ? n + skip_z : kNone;
+      }
+    };
+    auto weights_request = [&](int u) {
+      const int step = min(pw.part + wave * S + pw.i + u, KS - 1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        // where a row may end inside a step, the whole offset is the one that the
+        // range check sees
+        const int at = RAG && wrow[t] != kNone ? wrow[t] + step * 64 : wrow[t];
+        wq[u][t] = buf_load16(rw, (uint32_t)at, RAG ? 0 : (uint32_t)step * 64);
+      }
+    };
+    auto scale_step = [&](const Pos& p) {
+      const int step = p.part + wave * S + p.i;
+      return one_scale ? 0 : step < KS ? step : 0;
+    };
+    int salign[NT], zalign[NT];  // the windows' bytes inside their first dword
+    auto scales_request = [&] {
+      const int c = scale_step(ps) * SG;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const bool on = srow[t] != kNone;
+        const int so = RAG && on ? srow[t] + c * SB : srow[t];
+        const int zo = ZRAG && on ? zrow[t] + c : zrow[t];
+        sn[t].load(rs, so, RAG ? 0 : c * SB);
+        if constexpr (FMT == W4_INT) zn[t].load(rz, zo, ZRAG ? 0 : c);
+        salign[t] = so;
+        zalign[t] = zo;
+      }
+      if (next_round(ps)) scale_rows();
+    };
+    auto scales_take = [&] {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        sc[t] = sn[t];
+        sc[t].align(salign[t]);
+        if constexpr (FMT == W4_INT) {
+          zc[t] = zn[t];
+          zc[t].align(zalign[t]);
+        }
+      }
+    };
+
+    // tokens' elements in segments of 512, one a wave at a time
+    X8<XE> xr[2];
+    auto seg_request = [&](X8<XE>& x, int seg, int k0) {
+      const int m = seg * inv_s >> 16;
+      const bool on = m < nt;  // else an empty buffer
+      const uint32_t r = on ? route(m0 + m) : 0;
+      const size_t row = a.x_per_route || a.top_k == 1 ? r : __umulhi(r, a.inv_top_k);
+      const __amdgpu_buffer_rsrc_t rx =
+          make_rsrc(static_cast<const uint8_t*>(a.x) + row * a.K * elem_bytes(XE),
+                    on ? (uint32_t)a.K * elem_bytes(XE) : 0);
+      const uint32_t at = (uint32_t)(k0 + (seg - m * S) * kUnit + lane * 8) * elem_bytes(XE);
+      x.v[0] = buf_load16(rx, at, 0);  // zeros past K
+      if constexpr (XE == ELEM_F32) x.v[1] = buf_load16(rx, at + 16, 0);
+    };
+    auto seg_store = [&](const X8<XE>& x, int seg) {
+      const int m = seg * inv_s >> 16;
+      if (m >= nt) return;
+      uint32_t b[P][8];
+      split8<XE>(x, b);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        uint4 v;
+        if constexpr (FMT == W4_MX)
+          v = make_uint4(b[p][0] | b[p][1] << 16, b[p][2] | b[p][3] << 16,
+                         b[p][4] | b[p][5] << 16, b[p][6] | b[p][7] << 16);
+        else
+          v = make_uint4(b[p][0] | b[p][4] << 16, b[p][1] | b[p][5] << 16,
+                         b[p][2] | b[p][6] << 16, b[p][3] | b[p][7] << 16);
+        *reinterpret_cast<uint4*>(xs + (size_t)(p * nt + m) * xrow + (seg - m * S) * kUnit +
+                                  lane * 8) = v;
+      }
+    };
+    auto stage = [&](int k0, bool begun) {
+      const int segs = nt * S;
+      for (int seg = wave; seg < segs; seg += 2 * kWaves) {
+        if (!begun) {
+          seg_request(xr[0], seg, k0);
+          seg_request(xr[1], seg + kWaves, k0);
+        }
+        begun = false;
+        seg_store(xr[0], seg);
+        seg_store(xr[1], seg + kWaves);
+      }
+    };
+
+    f32x4 acc[NT];
+    // step i of the wave in this part, u in its round; `step` in the row
+    auto consume = [&](int u, int i, int step) {
+      const uint16_t* xp = xa + (wave * S + i) * 128;
+      bf16x8 xf[P][4];
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          xf[p][d] = *reinterpret_cast<const bf16x8*>(
+              xp + (size_t)p * nt * xrow + (GM == 1 ? 32 * g + 8 * d : 32 * d + 8 * g));
+      if constexpr (FMT == W4_MX) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          // the whole offset in the checked one: behind the last row's end it reads 0
-          wq[slot][t] = buf_load16(rw, wrow[t] + (uint32_t)step * 64, 0);
-          if constexpr (FMT == W4_MX) {
-            const int c = step * 4 + g;
-            sq[slot][t][0] = (uint32_t)buf_loadu8(rs, c < KG ? srow[t] + c : kNone, 0);
-          } else {
+          // 2^(c - 127) as a float: c in the exponent field, 0 subnormal, 255 NaN;
+          // past the row's end 0, as the tokens there
+          const uint32_t c = sc[t].d[u] >> (8 * g) & 0xFFu;
+          float s = __uint_as_float(c == 255 ? 0x7FC00000u : c ? c << 23 : 0x00400000u);
+          if (RAG && step * 4 + g >= KG) s = 0.f;
+          const uint32_t q[4] = {wq[u][t].x, wq[u][t].y, wq[u][t].z, wq[u][t].w};
 #pragma unroll
-            for (int q = 0; q < GM; ++q) {
-              const int c = GM > 1 ? step * GM + q : a.group == 128 ? step : 0;
-              sq[slot][t][q] = (uint32_t)buf_loadu16(rs, c < KG ? (srow[t] + c) * 2 : kNone, 0);
-              zq[slot][t][q] =
-                  has_zero ? (uint32_t)buf_loadu8(rz, c < KG ? srow[t] + c : kNone, 0) : 8u;
-            }
+          for (int d = 0; d < 4; ++d) {
+            const bf16x8 b = e2m1_to_bf16(q[d], s);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, acc[t], 0, 0, 0);
           }
         }
-      };
+      } else {
+        const bf16x8 ones = __builtin_bit_cast(bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u,
+                                                                 0x3F803F80u, 0x3F803F80u));
+        constexpr int DG = 4 / GM;  // instructions of one group
+        f32x4 sx[GM];
 #pragma unroll
-      for (int u = 0; u < kDepth; ++u)
-        if (u < S) request(u, u);
+        for (int q = 0; q < GM; ++q) {
+          sx[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int d = q * DG; d < (q + 1) * DG; ++d)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+              sx[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], ones, sx[q], 0, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          uint4 w = wq[u][t];
+          if constexpr (GM > 1) transpose4(w);
+          const uint32_t q4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int q = 0; q < GM; ++q) {
+            f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int d = q * DG; d < (q + 1) * DG; ++d) {
+              const bf16x8 b = int4_to_bf16(q4[d]);
+#pragma unroll
+              for (int p = 0; p < P; ++p)
+                v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, v, 0, 0, 0);
+            }
+            float s = bits_to_f32(one_scale ? sc[t].u16(0) : sc[t].u16(u * GM + q), a.scale_elem);
+            const float z = z0 + (float)(one_scale ? zc[t].u8(0) : zc[t].u8(u * GM + q));
+            if (RAG && !one_scale && step * GM + q >= KG) s = 0.f;  // past the row's end
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][j] += s * (v[j] - z * sx[q][j]);
+          }
+        }
+      }
+    };
 
-      if (m0 || k0) __syncthreads();  // the earlier part is read
-      const int per = kc / 8;
-      for (int u = tid; u < nt * per; u += kThreads) {
-        const int m = u / per, k = k0 + (u - m * per) * 8;
-        uint32_t b[P][8];
-        if (k < a.K) {
-          const int r = a.ids ? list[m0 + m] : first + m0 + m;
-          const int row = a.x_per_route ? r : r / a.top_k;
-          split8<XE>(static_cast<const uint8_t*>(a.x) +
-                         ((size_t)row * a.K + k) * elem_bytes(XE), b);
-        } else {
+    // the tokens' loads go first: loads return in order, so they are waited for
+    // while the weights are still on their way
+    seg_request(xr[0], wave, 0);
+    seg_request(xr[1], wave + kWaves, 0);
+    scale_rows();
+    scales_request();
+    weight_rows();
 #pragma unroll
-          for (int p = 0; p < P; ++p)
+    for (int u = 0; u < D; ++u) weights_request(u);
+    if (next_round(pw)) weight_rows();
+    if (m0) __syncthreads();  // the earlier tokens are read
+    stage(0, true);
+    __syncthreads();
+
+    for (int ti = tile0; ti < tile1; ++ti) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) b[p][i] = 0;
+      for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int part = 0; part < KS; part += S * kWaves) {
+        if (!whole && (part || ti > tile0)) {
+          __syncthreads();
+          stage(part * 128, false);
+          __syncthreads();
         }
+        for (int i = 0; i < S; i += D) {
+          scales_take();
+          scales_request();
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          uint4 v;
-          if constexpr (FMT == W4_MX)
-            v = make_uint4(b[p][0] | b[p][1] << 16, b[p][2] | b[p][3] << 16,
-                           b[p][4] | b[p][5] << 16, b[p][6] | b[p][7] << 16);
-          else
-            v = make_uint4(b[p][0] | b[p][4] << 16, b[p][1] | b[p][5] << 16,
-                           b[p][2] | b[p][6] << 16, b[p][3] | b[p][7] << 16);
-          *reinterpret_cast<uint4*>(xs + (size_t)(p * nt + m) * xrow + (k - k0)) = v;
+          for (int u = 0; u < D; ++u) {
+            const int step = part + wave * S + i + u;
+            if (step < KS) consume(u, i + u, step);
+            weights_request(u);
+          }
+          if (next_round(pw)) weight_rows();
         }
+      }
+      // the waves' sums: the others' through LDS to the first, which writes
+      if (wave) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (4 * g < nt)
+            *reinterpret_cast<f32x4*>(red + (((wave - 1) * NT + t) * 64 + lane) * 4) = acc[t];
       }
       __syncthreads();
-
-      for (int i0 = 0; i0 < S; i0 += kDepth) {
+      if (wave == 0 && 4 * g < nt) {
 #pragma unroll
-        for (int u = 0; u < kDepth; ++u) {
-          const int i = i0 + u;
-          if (i >= S || (k0 / 128) + i * kWaves + wave >= KS) continue;
-          const uint16_t* xp = xa + (i * kWaves + wave) * 128;
-          bf16x8 xf[P][4];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int p = 0; p < P; ++p)
+          for (int v = 0; v < kWaves - 1; ++v)
+            acc[t] += *reinterpret_cast<const f32x4*>(red + ((v * NT + t) * 64 + lane) * 4);
 #pragma unroll
-            for (int d = 0; d < 4; ++d)
-              xf[p][d] = *reinterpret_cast<const bf16x8*>(
-                  xp + (size_t)p * nt * xrow + (GM == 1 ? 32 * g + 8 * d : 32 * d + 8 * g));
-          if constexpr (FMT == W4_MX) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint32_t c = sq[u][t][0];
-              // 2^(c - 127) as a float: c in the exponent field, 0 subnormal, 255 NaN
-              const float s = __uint_as_float(c == 255 ? 0x7FC00000u : c ? c << 23 : 0x00400000u);
-              const uint32_t q[4] = {wq[u][t].x, wq[u][t].y, wq[u][t].z, wq[u][t].w};
-#pragma unroll
-              for (int d = 0; d < 4; ++d) {
-                const bf16x8 b = e2m1_to_bf16(q[d], s);
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                  acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, acc[t], 0, 0, 0);
-              }
-            }
+        for (int j = 0; j < 4; ++j) {
+          const int m = 4 * g + j;
+          if (m >= nt) break;
+          const int r = a.ids ? list[m0 + m] : first + m0 + m;
+          const size_t at = (size_t)r * out_n + ti * kCols + n16;
+          if constexpr (SWIGLU) {
+            if (ti * 16 + n16 < out_n) store_out(a.out, at, swiglu(acc[0][j], acc[NT - 1][j]), a.oelem);
           } else {
-            const bf16x8 ones = __builtin_bit_cast(bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u,
-                                                                     0x3F803F80u, 0x3F803F80u));
-            constexpr int DG = 4 / GM;  // instructions of one group
-            f32x4 sx[GM];
 #pragma unroll
-            for (int q = 0; q < GM; ++q) {
-              sx[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int d = q * DG; d < (q + 1) * DG; ++d)
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                  sx[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], ones, sx[q], 0, 0, 0);
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              if constexpr (GM > 1) transpose4(wq[u][t]);
-              const uint32_t q4[4] = {wq[u][t].x, wq[u][t].y, wq[u][t].z, wq[u][t].w};
-#pragma unroll
-              for (int q = 0; q < GM; ++q) {
-                f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int d = q * DG; d < (q + 1) * DG; ++d) {
-                  const bf16x8 b = int4_to_bf16(q4[d]);
-#pragma unroll
-                  for (int p = 0; p < P; ++p)
-                    v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, v, 0, 0, 0);
-                }
-                const float s = bits_to_f32(sq[u][t][q], a.scale_elem);
-                const float z = 128.f + (float)zq[u][t][q];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[t][j] += s * (v[j] - z * sx[q][j]);
-              }
-            }
+            for (int t = 0; t < NT; ++t)
+              if (ti * kCols + 16 * t + n16 < out_n) store_out(a.out, at + 16 * t, acc[t][j], a.oelem);
           }
-          if (i + kDepth < S) request(u, i + kDepth);
         }
       }
-    }
-
-    // the waves' sums, then one thread per output
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      *reinterpret_cast<f32x4*>(red + ((wave * NT + t) * 64 + lane) * 4) = acc[t];
-    __syncthreads();
-    auto total = [&](int t, int m, int c) {
-      float s = 0.f;
-#pragma unroll
-      for (int v = 0; v < kWaves; ++v)
-        s += red[((v * NT + t) * 64 + c + 16 * (m >> 2)) * 4 + (m & 3)];
-      return s;
-    };
-    for (int o = tid; o < nt * kCols; o += kThreads) {
-      const int m = o / kCols, c = o % kCols;
-      if (col0 + c >= out_n) continue;
-      const int r = a.ids ? list[m0 + m] : first + m0 + m;
-      const float v = SWIGLU ? swiglu(total(0, m, c), total(NT - 1, m, c)) : total(c / 16, m, c % 16);
-      store_out(a.out, (size_t)r * out_n + col0 + c, v, a.oelem);
+      if (ti + 1 < tile1) __syncthreads();
     }
   }
 }
@@ -391,45 +576,67 @@ k_w4_combine(const float* __restrict__ y, const int32_t* __restrict__ ids,
   store_out(out, at + 3, s.w, oelem);
 }
 
-// LDS of the tokens: a few tokens' whole K, or 1,024 elements of kTile tokens
-// (half as many of two parts).
-constexpr int kTokenLds = 33 * 1024;
-static_assert(kTile * (kUnit + kPad) * 2 <= kTokenLds, "one step of a full tile fits");
-static_assert(kWaves * 2 * 64 * 16 <= kTokenLds, "the waves' sums fit");
-
-template <int FMT, int XE, int GM, int NT, bool SWIGLU>
-hipError_t launch_one(const W4Args& a, hipStream_t stream) {
-  // tokens of one pass: 16, or 8 of two parts so that the LDS stays small
-  const int most = parts<XE>() == 1 ? kTile : kTile / 2;
-  const int tokens = a.R / a.top_k;
-  const int tile = tokens < most ? tokens : most;
+template <int FMT, int XE, int GM, bool RAG, int NT, bool SWIGLU, int D>
+hipError_t launch_one(const W4Args& a, int tile, hipStream_t stream) {
   const int out_n = SWIGLU ? a.N / 2 : a.N, cols = SWIGLU ? 16 : 16 * NT;
-  const int lists = a.ids ? (a.R * 2 + 15) / 16 * 16 : 0;
+  const int tiles = (out_n + cols - 1) / cols;
   const int y = !a.ids ? (a.R + tile - 1) / tile : a.R <= a.E ? a.R : a.E + 1;
-  hipLaunchKernelGGL((k_w4<FMT, XE, GM, NT, SWIGLU>), dim3((out_n + cols - 1) / cols, y),
-                     dim3(kThreads), kTokenLds + lists, stream, a, tile, kTokenLds);
+  // several tiles a workgroup once there are more workgroups than the GPU holds
+  const int64_t all = (int64_t)tiles * y;
+  const int run = all < 4096 ? 1 : all < 8192 ? 2 : 4;
+  const int lds = kTokenLds + (kWaves - 1) * NT * 1024 + (a.ids ? (a.R * 2 + 15) / 16 * 16 : 0);
+  hipLaunchKernelGGL((k_w4<FMT, XE, GM, RAG, NT, SWIGLU, D>), dim3((tiles + run - 1) / run, y),
+                     dim3(kThreads), lds, stream, a, tile, run);
   return hipGetLastError();
 }
 
-template <int FMT, int XE, int GM>
-hipError_t launch_shape(const W4Args& a, hipStream_t stream) {
-  if constexpr (XE != ELEM_F32)
-    if (a.swiglu) return launch_one<FMT, XE, GM, 2, true>(a, stream);
-  return launch_one<FMT, XE, GM, 1, false>(a, stream);
+template <int FMT, int XE, int GM, bool RAG, bool DEEP>
+hipError_t launch_shape(const W4Args& a, int tile, hipStream_t stream) {
+  if constexpr (XE == ELEM_F32) {
+    return launch_one<FMT, XE, GM, RAG, 2, false, DEEP ? 4 : 2>(a, tile, stream);
+  } else {
+    if (a.swiglu) return launch_one<FMT, XE, GM, RAG, 2, true, DEEP ? 4 : 2>(a, tile, stream);
+    return launch_one<FMT, XE, GM, RAG, 1, false, DEEP ? 4 : 2>(a, tile, stream);
+  }
+}
+
+template <int FMT, int XE, int GM, bool RAG>
+hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
+  // Tokens of one pass over the weights: 16, or 8 of two parts, so that two
+  // steps of them fit the LDS.  Where an expert has two routes or fewer on
+  // average, passes of half as many leave room for more steps ahead.
+  const int tokens = a.R / a.top_k;
+  int tile = kTile / parts<XE>();
+  if (a.ids && a.R <= 2 * (int64_t)a.E) tile /= 2;
+  if (tokens < tile) tile = tokens;
+  const int rounds = ((a.K + kUnit - 1) / kUnit + 3) / 4;
+  const bool whole = (kTokenLds / (parts<XE>() * tile * 2) - kPad) / kUnit >= 4 * rounds;
+  if (whole) return launch_shape<FMT, XE, GM, RAG, true>(a, tile, stream);
+  return launch_shape<FMT, XE, GM, RAG, false>(a, tile, stream);
 }
 
 template <int XE>
 hipError_t launch_format(int format, const W4Args& a, hipStream_t stream) {
-  if (format == W4_MX) return launch_shape<W4_MX, XE, 1>(a, stream);
-  if (a.group == 32) return launch_shape<W4_INT, XE, 4>(a, stream);
-  if (a.group == 64) return launch_shape<W4_INT, XE, 2>(a, stream);
-  return launch_shape<W4_INT, XE, 1>(a, stream);
+  const bool ragged = a.K % 512 || a.group == a.K;
+  if (format == W4_MX)
+    return ragged ? launch_walk<W4_MX, XE, 1, true>(a, stream)
+                  : launch_walk<W4_MX, XE, 1, false>(a, stream);
+  if (a.group == 32)
+    return ragged ? launch_walk<W4_INT, XE, 4, true>(a, stream)
+                  : launch_walk<W4_INT, XE, 4, false>(a, stream);
+  if (a.group == 64)
+    return ragged ? launch_walk<W4_INT, XE, 2, true>(a, stream)
+                  : launch_walk<W4_INT, XE, 2, false>(a, stream);
+  return ragged ? launch_walk<W4_INT, XE, 1, true>(a, stream)
+                : launch_walk<W4_INT, XE, 1, false>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_w4(int format, const W4Args& a, hipStream_t stream) {
-  if (a.R == 0) return hipSuccess;
+hipError_t launch_w4(int format, const W4Args& args, hipStream_t stream) {
+  if (args.R == 0) return hipSuccess;
+  W4Args a = args;
+  a.inv_top_k = (uint32_t)(((uint64_t(1) << 32) + a.top_k - 1) / a.top_k);
   if (a.xelem == ELEM_F32) return launch_format<ELEM_F32>(format, a, stream);
   if (a.xelem == ELEM_F16) return launch_format<ELEM_F16>(format, a, stream);
   return launch_format<ELEM_BF16>(format, a, stream);
