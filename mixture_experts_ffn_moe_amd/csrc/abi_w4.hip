@@ -81,7 +81,7 @@ int moe_w4_matvec(int32_t format, int32_t elem, const void* x, int32_t x_per_rou
     return rc;
   W4Args a{x, static_cast<const uint8_t*>(w), w_scale, w_zero, topk_ids, out,
            (int)K, (int)N, E, (int)(T * top_k), top_k, group ? group : (int)K,
-           elem, elem, elem, x_per_route != 0, swiglu != 0};
+           elem, elem, elem, x_per_route != 0, swiglu != 0, 0};
   return launched(launch_w4(format, a, static_cast<hipStream_t>(stream)));
 }
 
@@ -118,19 +118,17 @@ int fused_moe_w4(int32_t format, int32_t elem, const void* x, const void* w1, co
                     workspace ? workspace_bytes : (size_t)0, need);
   if (!aligned(workspace)) return abi_fail(MOE_ERR_ALIGN, "the workspace must be 16-byte aligned");
   const int R = (int)(T * top_k), I = (int)(N / 2);
-  float* h = static_cast<float*>(workspace);
-  float* y = h + up256((size_t)R * I * 4) / 4;
+  void* h = workspace;  // (R, 2, I) bf16 parts
+  float* y = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256((size_t)R * I * 4));
   hipStream_t s = static_cast<hipStream_t>(stream);
   W4Args up{x, static_cast<const uint8_t*>(w1), w1_scale, w1_zero, topk_ids, h,
             (int)K, (int)N, E, R, top_k, group ? group : (int)K,
-            elem, ELEM_F32, elem, 0, 1};
-  W4Args down{h, static_cast<const uint8_t*>(w2), w2_scale, w2_zero, topk_ids, y,
+            elem, ELEM_PARTS, elem, 0, 1, 0};
+  W4Args down{h, static_cast<const uint8_t*>(w2), w2_scale, w2_zero, topk_ids, out,
               I, (int)K, E, R, top_k, group ? group : I,
-              ELEM_F32, ELEM_F32, elem, 1, 0};
+              ELEM_PARTS, elem, elem, 1, 0, 0};
   hipError_t e = launch_w4(format, up, s);
-  if (e == hipSuccess) e = launch_w4(format, down, s);
-  if (e == hipSuccess)
-    e = launch_w4_combine(y, topk_ids, topk_weights, out, elem, (int)T, top_k, (int)K, E, s);
+  if (e == hipSuccess) e = launch_w4_down(format, down, topk_weights, y, (int)T, s);
   return launched(e);
 }
 

@@ -16,8 +16,10 @@
 //         the output.
 //   e2m1: the hardware's conversion, scale included; e2m1 times a power of
 //         two is a bf16, so this is exact too.
-// Activations are bf16 operands: bf16 ones as they are, fp16 and fp32 ones as
-// two bf16 parts hi + lo (exact for fp16, 2^-17 for fp32).
+// Activations are bf16 operands: bf16 ones as they are, fp16 ones as two bf16
+// parts hi + lo, which is exact.  The FFN's intermediate, an fp32 value, is
+// written as two such parts (2^-17 of it is lost), in the order the second
+// product reads.
 //
 // A 16x16x32 matrix instruction takes 16 tokens (A rows) and 16 weight rows (B
 // columns); a lane (n = l % 16, g = l / 16) reads 16 bytes of row n in each
@@ -96,37 +98,59 @@ __device__ __forceinline__ void transpose4(uint4& c) {
   c = make_uint4(e[0], e[1], f[0], f[1]);
 }
 
-// 8 consecutive activations of a lane: one 16-byte load, or two of fp32.
+// 8 consecutive activations of a lane: one 16-byte load, or one of each part.
 template <int XE>
 struct X8 {
-  uint4 v[XE == ELEM_F32 ? 2 : 1];
+  uint4 v[XE == ELEM_PARTS ? 2 : 1];
 };
 
-// Their bf16 bits: part 0 the nearest bf16, part 1 what is left.
+// From k of a row of K.
 template <int XE>
-__device__ __forceinline__ void split8(const X8<XE>& x, uint32_t (&b)[parts<XE>()][8]) {
+__device__ __forceinline__ void load_tokens(X8<XE>& x, __amdgpu_buffer_rsrc_t r, uint32_t k,
+                                            uint32_t K) {
+  x.v[0] = buf_load16(r, k < K ? k * 2 : 0xFFFFFFF0u, 0);  // zeros past K
+  if constexpr (XE == ELEM_PARTS) x.v[1] = buf_load16(r, k < K ? (K + k) * 2 : 0xFFFFFFF0u, 0);
+}
+
+// The place of element i of a row in the order that the weights' codes come in:
+// in each eight 0 4 1 5 2 6 3 7 for int4.
+template <int FMT>
+__device__ __forceinline__ int place_of(int i) {
+  return FMT == W4_MX ? i : (i & ~7) | (i & 3) << 1 | (i >> 2 & 1);
+}
+
+__device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return (a & 0xFFFFu) | b << 16; }
+__device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return a >> 16 | (b & 0xFFFF0000u); }
+
+// 8 activations into LDS as bf16 in that order, part 1 `part` elements after
+// part 0.
+template <int FMT, int XE>
+__device__ __forceinline__ void store_tokens(const X8<XE>& x, uint16_t* to, int part) {
+  if constexpr (XE == ELEM_PARTS) {  // in order already
+    *reinterpret_cast<uint4*>(to) = x.v[0];
+    *reinterpret_cast<uint4*>(to + part) = x.v[1];
+    return;
+  }
   const uint32_t d[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w};
-  if constexpr (XE == ELEM_BF16) {
+  uint32_t b[2][4];  // pairs of consecutive elements
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[0][2 * i] = d[i] & 0xFFFFu, b[0][2 * i + 1] = d[i] >> 16;
-  } else {
-    float f[8];
+  for (int i = 0; i < 4; ++i) {
+    b[0][i] = d[i], b[1][i] = 0;
     if constexpr (XE == ELEM_F16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bits_to_f32(d[i] & 0xFFFFu, ELEM_F16);
-        f[2 * i + 1] = bits_to_f32(d[i] >> 16, ELEM_F16);
-      }
-    } else {
-      const uint32_t u[4] = {x.v[1].x, x.v[1].y, x.v[1].z, x.v[1].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(d[i]), f[4 + i] = __uint_as_float(u[i]);
+      const float f = bits_to_f32(d[i] & 0xFFFFu, ELEM_F16), h = bits_to_f32(d[i] >> 16, ELEM_F16);
+      const uint32_t f0 = f32_to_bf16(f), h0 = f32_to_bf16(h);
+      b[0][i] = f0 | h0 << 16;
+      b[1][i] = (uint32_t)f32_to_bf16(f - __uint_as_float(f0 << 16)) |
+                (uint32_t)f32_to_bf16(h - __uint_as_float(h0 << 16)) << 16;
     }
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      b[0][i] = f32_to_bf16(f[i]);
-      b[1][i] = f32_to_bf16(f[i] - __uint_as_float(b[0][i] << 16));
-    }
+  for (int p = 0; p < parts<XE>(); ++p) {
+    uint4 v = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
+    if constexpr (FMT != W4_MX)
+      v = make_uint4(lo_halves(b[p][0], b[p][2]), hi_halves(b[p][0], b[p][2]),
+                     lo_halves(b[p][1], b[p][3]), hi_halves(b[p][1], b[p][3]));
+    *reinterpret_cast<uint4*>(to + p * part) = v;
   }
 }
 
@@ -176,6 +200,93 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dword_rsrc(const uint8_t* p, u
   return make_rsrc(p - skip, bytes ? (bytes + skip + 3) & ~3u : 0);
 }
 
+// The table's scales of a row in a step, and their bytes.
+template <int FMT, int GM>
+constexpr int step_scales() { return FMT == W4_MX ? 4 : GM; }
+template <int FMT>
+constexpr int scale_bytes() { return FMT == W4_MX ? 1 : 2; }
+
+// Zero points of D steps: two are no whole dword, so they can lie anywhere too.
+template <int D, int GM, bool RAG>
+using ZeroWindow = Window<D * GM, RAG || D * GM % 4 != 0>;
+template <int FMT, int D, int GM, bool RAG>
+using ScaleWindow = Window<D * step_scales<FMT, GM>() * scale_bytes<FMT>(), RAG>;
+
+// acc[t] += tokens x weights of one 128-wide step, the u-th of its window.
+// xp: the lane's token at this step in LDS, the parts `part` elements apart.
+// valid: the scale groups of the step that the row has (RAG).
+template <int FMT, int GM, bool RAG, int P, int NT, int D>
+__device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* xp, int part,
+                                             const uint4 (&wq)[NT],
+                                             const ScaleWindow<FMT, D, GM, RAG> (&sc)[NT],
+                                             const ZeroWindow<D, GM, RAG> (&zc)[NT], int u,
+                                             int valid, bool one_scale, float z0, int scale_elem) {
+  const int g = (threadIdx.x & 63) >> 4;
+  bf16x8 xf[P][4];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      xf[p][d] = *reinterpret_cast<const bf16x8*>(
+          xp + p * part + (GM == 1 ? 32 * g + 8 * d : 32 * d + 8 * g));
+  if constexpr (FMT == W4_MX) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      // 2^(c - 127) as a float: c in the exponent field, 0 subnormal, 255 NaN;
+      // past the row's end 0, as the tokens there
+      const uint32_t c = sc[t].d[u] >> (8 * g) & 0xFFu;
+      float s = __uint_as_float(c == 255 ? 0x7FC00000u : c ? c << 23 : 0x00400000u);
+      if (RAG && g >= valid) s = 0.f;
+      const uint32_t q[4] = {wq[t].x, wq[t].y, wq[t].z, wq[t].w};
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const bf16x8 b = e2m1_to_bf16(q[d], s);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, acc[t], 0, 0, 0);
+      }
+    }
+  } else {
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u,
+                                                             0x3F803F80u, 0x3F803F80u));
+    constexpr int DG = 4 / GM;  // instructions of one group
+    f32x4 sx[GM];
+#pragma unroll
+    for (int q = 0; q < GM; ++q) {
+      sx[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int d = q * DG; d < (q + 1) * DG; ++d)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          sx[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], ones, sx[q], 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint4 w = wq[t];
+      if constexpr (GM > 1) transpose4(w);
+      const uint32_t q4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int q = 0; q < GM; ++q) {
+        f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int d = q * DG; d < (q + 1) * DG; ++d) {
+          const bf16x8 b = int4_to_bf16(q4[d]);
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, v, 0, 0, 0);
+        }
+        float s = bits_to_f32(one_scale ? sc[t].u16(0) : sc[t].u16(u * GM + q), scale_elem);
+        const float z = z0 + (float)(one_scale ? zc[t].u8(0) : zc[t].u8(u * GM + q));
+        if (RAG && !one_scale && q >= valid) s = 0.f;  // past the row's end
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][j] += s * (v[j] - z * sx[q][j]);
+      }
+    }
+  }
+}
+
+constexpr int kNone = (int)0x80000000;  // past every buffer
+
 // GM: scale groups in a 128-wide step (int4: 1, 2, 4).  RAG: K is no multiple of
 // 512 or a row has one scale, so that the scales of D steps lie at any address,
 // and a row may end inside a step.  NT: 16-row weight tiles taken together; with SWIGLU the
@@ -187,6 +298,7 @@ template <int FMT, int XE, int GM, bool RAG, int NT, bool SWIGLU, int D>
 __global__ void __launch_bounds__(kThreads, GM > 1 ? 2 : NT == 2 && D == 4 && (RAG || XE != ELEM_BF16) ? 3 : 4)
 k_w4(W4Args a, int tile, int run) {
   constexpr int P = parts<XE>();
+  constexpr int kRowParts = XE == ELEM_PARTS ? 2 : 1;  // 16-bit rows of a token in memory
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* xs = reinterpret_cast<uint16_t*>(smem);
   float* red = reinterpret_cast<float*>(smem + kTokenLds);  // waves 1.. of each tile
@@ -246,7 +358,8 @@ k_w4(W4Args a, int tile, int run) {
       if (count) lead = list[0];
     }
     if (count == 0 || (a.R <= a.E && lead != y)) return;
-    if (e < 0) {  // routes without an expert here: zeros
+    if (e < 0) {  // routes without an expert here: zeros (parts are not read)
+      if (a.oelem == ELEM_PARTS) return;
       if (few) __syncthreads();
       const int c0 = tile0 * kCols, w = min(out_n, tile1 * kCols) - c0;
       for (int i = tid; i < count * w; i += kThreads)
@@ -266,8 +379,7 @@ k_w4(W4Args a, int tile, int run) {
   const uint32_t pitch = (uint32_t)a.K / 2;
   const __amdgpu_buffer_rsrc_t rw =
       make_rsrc(a.w + (size_t)e * a.N * pitch, (uint32_t)a.N * pitch);
-  constexpr int SB = FMT == W4_MX ? 1 : 2;       // bytes of a scale
-  constexpr int SG = FMT == W4_MX ? 4 : GM;      // scales of a row in a step
+  constexpr int SB = scale_bytes<FMT>(), SG = step_scales<FMT, GM>();
   int skip_s, skip_z;
   const __amdgpu_buffer_rsrc_t rs =
       dword_rsrc(static_cast<const uint8_t*>(a.scale) + (size_t)e * a.N * KG * SB,
@@ -292,11 +404,10 @@ k_w4(W4Args a, int tile, int run) {
     // order.  All are unconditional, so that the waits count them exactly: past
     // the last tile the rows lie outside the buffers (the loads return zeros and
     // touch no memory), past the last step the last one is read again.
-    constexpr int kNone = (int)0x80000000;  // past every buffer
     uint4 wq[D][NT];
-    Window<D * SG * SB, RAG> sn[NT], sc[NT];      // the next round's scales, this one's
-    constexpr bool ZRAG = RAG || D * GM % 4;      // two zero points are no whole dword
-    Window<D * GM, ZRAG> zn[NT], zc[NT];
+    ScaleWindow<FMT, D, GM, RAG> sn[NT], sc[NT];  // the next round's scales, this one's
+    ZeroWindow<D, GM, RAG> zn[NT], zc[NT];
+    constexpr bool ZRAG = RAG || D * GM % 4 != 0;
     int wrow[NT], srow[NT], zrow[NT];
     auto weight_row = [&](int t0, int t) {
       return SWIGLU ? t * out_n + min(t0 * 16 + n16, out_n - 1)
@@ -379,29 +490,14 @@ k_w4(W4Args a, int tile, int run) {
       const uint32_t r = on ? route(m0 + m) : 0;
       const size_t row = a.x_per_route || a.top_k == 1 ? r : __umulhi(r, a.inv_top_k);
       const __amdgpu_buffer_rsrc_t rx =
-          make_rsrc(static_cast<const uint8_t*>(a.x) + row * a.K * elem_bytes(XE),
-                    on ? (uint32_t)a.K * elem_bytes(XE) : 0);
-      const uint32_t at = (uint32_t)(k0 + (seg - m * S) * kUnit + lane * 8) * elem_bytes(XE);
-      x.v[0] = buf_load16(rx, at, 0);  // zeros past K
-      if constexpr (XE == ELEM_F32) x.v[1] = buf_load16(rx, at + 16, 0);
+          make_rsrc(static_cast<const uint16_t*>(a.x) + row * a.K * kRowParts,
+                    on ? (uint32_t)a.K * kRowParts * 2 : 0);
+      load_tokens<XE>(x, rx, k0 + (seg - m * S) * kUnit + lane * 8, a.K);
     };
     auto seg_store = [&](const X8<XE>& x, int seg) {
       const int m = seg * inv_s >> 16;
       if (m >= nt) return;
-      uint32_t b[P][8];
-      split8<XE>(x, b);
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        uint4 v;
-        if constexpr (FMT == W4_MX)
-          v = make_uint4(b[p][0] | b[p][1] << 16, b[p][2] | b[p][3] << 16,
-                         b[p][4] | b[p][5] << 16, b[p][6] | b[p][7] << 16);
-        else
-          v = make_uint4(b[p][0] | b[p][4] << 16, b[p][1] | b[p][5] << 16,
-                         b[p][2] | b[p][6] << 16, b[p][3] | b[p][7] << 16);
-        *reinterpret_cast<uint4*>(xs + (size_t)(p * nt + m) * xrow + (seg - m * S) * kUnit +
-                                  lane * 8) = v;
-      }
+      store_tokens<FMT, XE>(x, xs + (size_t)m * xrow + (seg - m * S) * kUnit + lane * 8, nt * xrow);
     };
     auto stage = [&](int k0, bool begun) {
       const int segs = nt * S;
@@ -417,71 +513,6 @@ k_w4(W4Args a, int tile, int run) {
     };
 
     f32x4 acc[NT];
-    // step i of the wave in this part, u in its round; `step` in the row
-    auto consume = [&](int u, int i, int step) {
-      const uint16_t* xp = xa + (wave * S + i) * 128;
-      bf16x8 xf[P][4];
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-          xf[p][d] = *reinterpret_cast<const bf16x8*>(
-              xp + (size_t)p * nt * xrow + (GM == 1 ? 32 * g + 8 * d : 32 * d + 8 * g));
-      if constexpr (FMT == W4_MX) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          // 2^(c - 127) as a float: c in the exponent field, 0 subnormal, 255 NaN;
-          // past the row's end 0, as the tokens there
-          const uint32_t c = sc[t].d[u] >> (8 * g) & 0xFFu;
-          float s = __uint_as_float(c == 255 ? 0x7FC00000u : c ? c << 23 : 0x00400000u);
-          if (RAG && step * 4 + g >= KG) s = 0.f;
-          const uint32_t q[4] = {wq[u][t].x, wq[u][t].y, wq[u][t].z, wq[u][t].w};
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const bf16x8 b = e2m1_to_bf16(q[d], s);
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, acc[t], 0, 0, 0);
-          }
-        }
-      } else {
-        const bf16x8 ones = __builtin_bit_cast(bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u,
-                                                                 0x3F803F80u, 0x3F803F80u));
-        constexpr int DG = 4 / GM;  // instructions of one group
-        f32x4 sx[GM];
-#pragma unroll
-        for (int q = 0; q < GM; ++q) {
-          sx[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int d = q * DG; d < (q + 1) * DG; ++d)
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-              sx[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], ones, sx[q], 0, 0, 0);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          uint4 w = wq[u][t];
-          if constexpr (GM > 1) transpose4(w);
-          const uint32_t q4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int q = 0; q < GM; ++q) {
-            f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int d = q * DG; d < (q + 1) * DG; ++d) {
-              const bf16x8 b = int4_to_bf16(q4[d]);
-#pragma unroll
-              for (int p = 0; p < P; ++p)
-                v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, v, 0, 0, 0);
-            }
-            float s = bits_to_f32(one_scale ? sc[t].u16(0) : sc[t].u16(u * GM + q), a.scale_elem);
-            const float z = z0 + (float)(one_scale ? zc[t].u8(0) : zc[t].u8(u * GM + q));
-            if (RAG && !one_scale && step * GM + q >= KG) s = 0.f;  // past the row's end
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[t][j] += s * (v[j] - z * sx[q][j]);
-          }
-        }
-      }
-    };
 
     // the tokens' loads go first: loads return in order, so they are waited for
     // while the weights are still on their way
@@ -512,7 +543,10 @@ k_w4(W4Args a, int tile, int run) {
 #pragma unroll
           for (int u = 0; u < D; ++u) {
             const int step = part + wave * S + i + u;
-            if (step < KS) consume(u, i + u, step);
+            if (step < KS)
+              step_product<FMT, GM, RAG, P, NT, D>(acc, xa + (wave * S + i + u) * 128, nt * xrow,
+                                                   wq[u], sc, zc, u, KG - step * SG, one_scale,
+                                                   z0, a.scale_elem);
             weights_request(u);
           }
           if (next_round(pw)) weight_rows();
@@ -539,7 +573,17 @@ k_w4(W4Args a, int tile, int run) {
           const int r = a.ids ? list[m0 + m] : first + m0 + m;
           const size_t at = (size_t)r * out_n + ti * kCols + n16;
           if constexpr (SWIGLU) {
-            if (ti * 16 + n16 < out_n) store_out(a.out, at, swiglu(acc[0][j], acc[NT - 1][j]), a.oelem);
+            const float v = swiglu(acc[0][j], acc[NT - 1][j]);
+            const int n = ti * 16 + n16;
+            if (n >= out_n) continue;
+            if (a.oelem == ELEM_PARTS) {
+              uint16_t* row = static_cast<uint16_t*>(a.out) + (size_t)r * out_n * 2 + place_of<FMT>(n);
+              const uint32_t hi = f32_to_bf16(v);
+              row[0] = (uint16_t)hi;
+              row[out_n] = f32_to_bf16(v - __uint_as_float(hi << 16));
+            } else {
+              store_out(a.out, at, v, a.oelem);
+            }
           } else {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -552,28 +596,144 @@ k_w4(W4Args a, int tile, int run) {
   }
 }
 
+// The second product and the weighted sum of one token at once: a workgroup has
+// 16 output columns of a token, and each wave one of the token's routes at a
+// time, over the whole of K.  Nothing goes through memory between the product
+// and the sum, and there is one launch less; an expert that two tokens chose is
+// read twice.  x (R, 2, K) in two parts.  Grid: x the columns, y the token.
+constexpr int kTokenWaves = 8;   // routes at once
+constexpr int kTokenPart = 2048; // K elements of a route in LDS at a time
+
+template <int FMT, int GM, bool RAG>
+__global__ void __launch_bounds__(kTokenWaves * 64, 2)
+k_w4_token(W4Args a, const float* __restrict__ weights) {
+  constexpr int D = 8, P = 2, SB = scale_bytes<FMT>(), SG = step_scales<FMT, GM>();
+  constexpr int xrow = kTokenPart;  // every lane reads the same token: no padding
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 63, wave = wave_id(), waves = blockDim.x / 64;
+  const int n16 = lane & 15, g = lane >> 4;
+  const int t = blockIdx.y, n = min((int)blockIdx.x * 16 + n16, a.N - 1);
+  uint16_t* xs = reinterpret_cast<uint16_t*>(smem) + (size_t)wave * P * xrow;
+  const int KS = (a.K + 127) / 128, KG = a.K / a.group;
+  const uint32_t pitch = (uint32_t)a.K / 2;
+  const bool has_zero = FMT == W4_INT && a.zero;
+  const float z0 = has_zero ? 128.f : 136.f;
+  const bool one_scale = GM == 1 && FMT == W4_INT && KG == 1;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+
+  for (int q = wave; q < a.top_k; q += waves) {
+    const int r = t * a.top_k + q;
+    const int e = a.ids[r];
+    if ((unsigned)e >= (unsigned)a.E) continue;
+    const __amdgpu_buffer_rsrc_t rx =
+        make_rsrc(static_cast<const uint16_t*>(a.x) + (size_t)r * a.K * 2, (uint32_t)a.K * 4);
+    const __amdgpu_buffer_rsrc_t rw =
+        make_rsrc(a.w + (size_t)e * a.N * pitch, (uint32_t)a.N * pitch);
+    int skip_s, skip_z;
+    const __amdgpu_buffer_rsrc_t rs =
+        dword_rsrc(static_cast<const uint8_t*>(a.scale) + (size_t)e * a.N * KG * SB,
+                   (uint32_t)a.N * KG * SB, skip_s);
+    const __amdgpu_buffer_rsrc_t rz = dword_rsrc(has_zero ? a.zero + (size_t)e * a.N * KG : a.w,
+                                                 has_zero ? (uint32_t)a.N * KG : 0, skip_z);
+    const int wrow = (int)((uint32_t)n * pitch + 16 * g);
+    const int srow = n * KG * SB + skip_s, zrow = n * KG + skip_z;
+
+    uint4 wq[D][1];
+    ScaleWindow<FMT, D, GM, RAG> sn[1], sc[1];
+    ZeroWindow<D, GM, RAG> zn[1], zc[1];
+    int salign = 0, zalign = 0;
+    auto weights_request = [&](int u, int step) {  // past the end the last one again
+      step = min(step, KS - 1);
+      wq[u][0] = buf_load16(rw, (uint32_t)(RAG ? wrow + step * 64 : wrow),
+                            RAG ? 0 : (uint32_t)step * 64);
+    };
+    auto scales_request = [&](int step) {
+      const int c = (one_scale || step >= KS ? 0 : step) * SG;
+      salign = RAG ? srow + c * SB : srow;
+      zalign = RAG ? zrow + c : zrow;
+      sn[0].load(rs, salign, RAG ? 0 : c * SB);
+      if constexpr (FMT == W4_INT) zn[0].load(rz, zalign, RAG ? 0 : c);
+    };
+    f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+    for (int k0 = 0; k0 < a.K; k0 += kTokenPart) {
+      X8<ELEM_PARTS> xr[kTokenPart / 512];
+#pragma unroll
+      for (int i = 0; i < kTokenPart / 512; ++i)
+        load_tokens<ELEM_PARTS>(xr[i], rx, k0 + i * 512 + lane * 8, a.K);
+      if (k0 == 0) {
+        scales_request(0);
+#pragma unroll
+        for (int u = 0; u < D; ++u) weights_request(u, u);
+      }
+#pragma unroll
+      for (int i = 0; i < kTokenPart / 512; ++i)
+        store_tokens<FMT, ELEM_PARTS>(xr[i], xs + i * 512 + lane * 8, xrow);
+      __builtin_amdgcn_wave_barrier();  // the wave's own LDS, in order
+      const int end = min(KS, (k0 + kTokenPart) / 128);
+      for (int s0 = k0 / 128; s0 < end; s0 += D) {
+        sc[0] = sn[0];
+        sc[0].align(salign);
+        if constexpr (FMT == W4_INT) {
+          zc[0] = zn[0];
+          zc[0].align(zalign);
+        }
+        scales_request(s0 + D);
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+          if (s0 + u < KS)
+            step_product<FMT, GM, RAG, P, 1, D>(acc, xs + (s0 + u) * 128 - k0, xrow, wq[u], sc, zc,
+                                                u, KG - (s0 + u) * SG, one_scale, z0,
+                                                a.scale_elem);
+          weights_request(u, s0 + u + D);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    sum += weights[r] * acc[0];
+  }
+  // token rows: only the first of the product's 16 is one
+  float* red = reinterpret_cast<float*>(smem);
+  __syncthreads();  // the tokens are read
+  if (g == 0) red[wave * 16 + n16] = sum[0];
+  __syncthreads();
+  const int c = blockIdx.x * 16 + threadIdx.x;
+  if (threadIdx.x < 16 && c < a.N) {
+    float v = 0.f;
+    for (int w = 0; w < waves; ++w) v += red[w * 16 + threadIdx.x];
+    store_out(a.out, (size_t)t * a.N + c, v, a.oelem);
+  }
+}
+
 constexpr int kCombineThreads = 256;
 
+// out[t] = the sum of w[r] y[r]; eight routes' ids, weights and rows are
+// requested before any is added.
 __global__ void __launch_bounds__(kCombineThreads)
 k_w4_combine(const float* __restrict__ y, const int32_t* __restrict__ ids,
              const float* __restrict__ w, void* __restrict__ out, int oelem, int top_k, int K,
              int E) {
+  constexpr int kBatch = 8;
   const int t = blockIdx.y, c = (blockIdx.x * kCombineThreads + threadIdx.x) * 4;
   if (c >= K) return;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int j = 0; j < top_k; ++j) {
-    const int r = t * top_k + j;
-    if ((unsigned)ids[r] >= (unsigned)E) continue;
-    const float wr = w[r];
-    const float4 v = *reinterpret_cast<const float4*>(y + (size_t)r * K + c);
-    s.x += wr * v.x, s.y += wr * v.y, s.z += wr * v.z, s.w += wr * v.w;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < top_k; j0 += kBatch) {
+    int id[kBatch];
+    float wr[kBatch];
+    f32x4 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = t * top_k + min(j0 + u, top_k - 1);
+      id[u] = ids[r];
+      wr[u] = w[r];
+      v[u] = *reinterpret_cast<const f32x4*>(y + (size_t)r * K + c);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (j0 + u < top_k && (unsigned)id[u] < (unsigned)E) s += wr[u] * v[u];
   }
   const size_t at = (size_t)t * K + c;
-  store_out(out, at, s.x, oelem);
-  store_out(out, at + 1, s.y, oelem);
-  store_out(out, at + 2, s.z, oelem);
-  store_out(out, at + 3, s.w, oelem);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) store_out(out, at + i, s[i], oelem);
 }
 
 template <int FMT, int XE, int GM, bool RAG, int NT, bool SWIGLU, int D>
@@ -592,7 +752,7 @@ hipError_t launch_one(const W4Args& a, int tile, hipStream_t stream) {
 
 template <int FMT, int XE, int GM, bool RAG, bool DEEP>
 hipError_t launch_shape(const W4Args& a, int tile, hipStream_t stream) {
-  if constexpr (XE == ELEM_F32) {
+  if constexpr (XE == ELEM_PARTS) {
     return launch_one<FMT, XE, GM, RAG, 2, false, DEEP ? 4 : 2>(a, tile, stream);
   } else {
     if (a.swiglu) return launch_one<FMT, XE, GM, RAG, 2, true, DEEP ? 4 : 2>(a, tile, stream);
@@ -637,15 +797,46 @@ hipError_t launch_w4(int format, const W4Args& args, hipStream_t stream) {
   if (args.R == 0) return hipSuccess;
   W4Args a = args;
   a.inv_top_k = (uint32_t)(((uint64_t(1) << 32) + a.top_k - 1) / a.top_k);
-  if (a.xelem == ELEM_F32) return launch_format<ELEM_F32>(format, a, stream);
+  if (a.xelem == ELEM_PARTS) return launch_format<ELEM_PARTS>(format, a, stream);
   if (a.xelem == ELEM_F16) return launch_format<ELEM_F16>(format, a, stream);
   return launch_format<ELEM_BF16>(format, a, stream);
 }
 
-hipError_t launch_w4_combine(const float* y, const int32_t* ids, const float* w, void* out,
-                             int oelem, int T, int top_k, int K, int E, hipStream_t stream) {
-  if (T == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_w4_combine, dim3((K / 4 + kCombineThreads - 1) / kCombineThreads, T),
-                     dim3(kCombineThreads), 0, stream, y, ids, w, out, oelem, top_k, K, E);
+namespace {
+
+template <int FMT, int GM>
+void launch_token(const W4Args& a, const float* weights, bool ragged, dim3 grid, int waves,
+                  size_t lds, hipStream_t stream) {
+  if (ragged)
+    hipLaunchKernelGGL((k_w4_token<FMT, GM, true>), grid, dim3(waves * 64), lds, stream, a, weights);
+  else
+    hipLaunchKernelGGL((k_w4_token<FMT, GM, false>), grid, dim3(waves * 64), lds, stream, a, weights);
+}
+
+}  // namespace
+
+hipError_t launch_w4_down(int format, const W4Args& a, const float* weights, float* y, int T,
+                          hipStream_t stream) {
+  // One token's routes seldom share an expert, so its weights are read once
+  // either way.
+  if (T <= kW4TokenMax) {
+    const int waves = a.top_k < kTokenWaves ? a.top_k : kTokenWaves;
+    const size_t lds = (size_t)waves * 2 * kTokenPart * 2;  // at most 64 KiB
+    const dim3 grid((a.N + 15) / 16, T);
+    const bool ragged = a.K % 512 || a.group == a.K;
+    if (format == W4_MX) launch_token<W4_MX, 1>(a, weights, ragged, grid, waves, lds, stream);
+    else if (a.group == 32) launch_token<W4_INT, 4>(a, weights, ragged, grid, waves, lds, stream);
+    else if (a.group == 64) launch_token<W4_INT, 2>(a, weights, ragged, grid, waves, lds, stream);
+    else launch_token<W4_INT, 1>(a, weights, ragged, grid, waves, lds, stream);
+    return hipGetLastError();
+  }
+  W4Args down = a;
+  down.out = y;
+  down.oelem = ELEM_F32;
+  const hipError_t e = launch_w4(format, down, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_w4_combine, dim3((a.N / 4 + kCombineThreads - 1) / kCombineThreads, T),
+                     dim3(kCombineThreads), 0, stream, y, a.ids, weights, a.out, a.oelem, a.top_k,
+                     a.N, a.E);
   return hipGetLastError();
 }
