@@ -66,6 +66,6 @@ hipError_t launch_w4(int format, const W4Args& a, hipStream_t stream);
 // The second product of the FFN and the weighted sum: a.x the intermediate (R,
 // 2, K) in parts, a.out (T, N), out[t] = sum over t's routes with an expert in [0, E) of
 // weights[r] W x[r].  y: R * N floats of workspace, unused at T <= kW4TokenMax.
-constexpr int kW4TokenMax = 1;
+constexpr int kW4TokenMax = 4;
 hipError_t launch_w4_down(int format, const W4Args& a, const float* weights, float* y, int T,
                           hipStream_t stream);

@@ -11,8 +11,10 @@
 //   int4: (v & 0x000F000F) | 0x43004300 holds 128 + q of two nibbles, exactly.
 //         The group's sum of (128 + q) x minus (128 + z) times the group's sum
 //         of x, times s, is the group's part; both sums are fp32, the second
-//         one from the same matrix instruction with ones for weights.  The
-//         offset costs about five of fp32's 24 bits, against the 8 or 11 of
+//         one from the same matrix instruction with ones for weights (the
+//         vector units are the busier ones; sums taken once, as the tokens are
+//         brought into LDS, cost 8 tokens of 4096 x 4096 10.2 us against 9.0).
+//         The offset costs about five of fp32's 24 bits, against the 8 or 11 of
 //         the output.
 //   e2m1: the hardware's conversion, scale included; e2m1 times a power of
 //         two is a bf16, so this is exact too.
@@ -122,17 +124,33 @@ __device__ __forceinline__ int place_of(int i) {
 __device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return (a & 0xFFFFu) | b << 16; }
 __device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return a >> 16 | (b & 0xFFFF0000u); }
 
+// v and what lane movement CTRL brings in, added
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+
+// Lanes of a 16-lane row that hold one scale group's 8-element shares (GM groups
+// in the row's 128 elements): every lane gets their sum.
+template <int GM>
+__device__ __forceinline__ float group_sum(float v) {
+  v = add_dpp<0xB1>(v);                         // neighbours
+  v = add_dpp<0x4E>(v);                         // quads
+  if constexpr (GM <= 2) v = add_dpp<0x141>(v);  // the half row's other quad
+  if constexpr (GM == 1) v = add_dpp<0x140>(v);  // the row's other half
+  return v;
+}
+
+__device__ __forceinline__ float pair_sum(uint32_t d) {
+  return __uint_as_float(d << 16) + __uint_as_float(d & 0xFFFF0000u);
+}
+
 // 8 activations into LDS as bf16 in that order, part 1 `part` elements after
-// part 0.
+// part 0.  Returns their sum (int4; in fp32 as every sum here).
 template <int FMT, int XE>
-__device__ __forceinline__ void store_tokens(const X8<XE>& x, uint16_t* to, int part) {
-  if constexpr (XE == ELEM_PARTS) {  // in order already
-    *reinterpret_cast<uint4*>(to) = x.v[0];
-    *reinterpret_cast<uint4*>(to + part) = x.v[1];
-    return;
-  }
+__device__ __forceinline__ float store_tokens(const X8<XE>& x, uint16_t* to, int part) {
   const uint32_t d[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w};
-  uint32_t b[2][4];  // pairs of consecutive elements
+  uint32_t b[2][4];  // pairs of elements
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     b[0][i] = d[i], b[1][i] = 0;
@@ -144,14 +162,21 @@ __device__ __forceinline__ void store_tokens(const X8<XE>& x, uint16_t* to, int 
                 (uint32_t)f32_to_bf16(h - __uint_as_float(h0 << 16)) << 16;
     }
   }
+  if constexpr (XE == ELEM_PARTS)  // in order already
+    b[1][0] = x.v[1].x, b[1][1] = x.v[1].y, b[1][2] = x.v[1].z, b[1][3] = x.v[1].w;
+  float sum = 0.f;
 #pragma unroll
   for (int p = 0; p < parts<XE>(); ++p) {
     uint4 v = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
-    if constexpr (FMT != W4_MX)
+    if constexpr (FMT != W4_MX && XE != ELEM_PARTS)
       v = make_uint4(lo_halves(b[p][0], b[p][2]), hi_halves(b[p][0], b[p][2]),
                      lo_halves(b[p][1], b[p][3]), hi_halves(b[p][1], b[p][3]));
     *reinterpret_cast<uint4*>(to + p * part) = v;
+    if constexpr (FMT != W4_MX)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += pair_sum(b[p][i]);
   }
+  return sum;
 }
 
 __device__ __forceinline__ void store_out(void* out, size_t at, float v, int elem) {
@@ -214,9 +239,12 @@ using ScaleWindow = Window<D * step_scales<FMT, GM>() * scale_bytes<FMT>(), RAG>
 
 // acc[t] += tokens x weights of one 128-wide step, the u-th of its window.
 // xp: the lane's token at this step in LDS, the parts `part` elements apart.
-// valid: the scale groups of the step that the row has (RAG).
-template <int FMT, int GM, bool RAG, int P, int NT, int D>
+// valid: the scale groups of the step that the row has (RAG).  ONE: every row
+// of the product is the same token, whose sum over group q of the step is sx[q];
+// only the first row is made.
+template <int FMT, int GM, bool RAG, int P, int NT, int D, bool ONE>
 __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* xp, int part,
+                                             const float* sx,
                                              const uint4 (&wq)[NT],
                                              const ScaleWindow<FMT, D, GM, RAG> (&sc)[NT],
                                              const ZeroWindow<D, GM, RAG> (&zc)[NT], int u,
@@ -247,18 +275,22 @@ __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* x
       }
     }
   } else {
-    const bf16x8 ones = __builtin_bit_cast(bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u,
-                                                             0x3F803F80u, 0x3F803F80u));
     constexpr int DG = 4 / GM;  // instructions of one group
-    f32x4 sx[GM];
+    f32x4 xsum[GM];
 #pragma unroll
     for (int q = 0; q < GM; ++q) {
-      sx[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      xsum[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (ONE) {
+        xsum[q][0] = sx[q];
+      } else {
+        const bf16x8 ones = __builtin_bit_cast(
+            bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u));
 #pragma unroll
-      for (int d = q * DG; d < (q + 1) * DG; ++d)
+        for (int d = q * DG; d < (q + 1) * DG; ++d)
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-          sx[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], ones, sx[q], 0, 0, 0);
+          for (int p = 0; p < P; ++p)
+            xsum[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], ones, xsum[q], 0, 0, 0);
+      }
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -279,7 +311,7 @@ __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* x
         const float z = z0 + (float)(one_scale ? zc[t].u8(0) : zc[t].u8(u * GM + q));
         if (RAG && !one_scale && q >= valid) s = 0.f;  // past the row's end
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][j] += s * (v[j] - z * sx[q][j]);
+        for (int j = 0; j < (ONE ? 1 : 4); ++j) acc[t][j] += s * (v[j] - z * xsum[q][j]);
       }
     }
   }
@@ -544,9 +576,9 @@ k_w4(W4Args a, int tile, int run) {
           for (int u = 0; u < D; ++u) {
             const int step = part + wave * S + i + u;
             if (step < KS)
-              step_product<FMT, GM, RAG, P, NT, D>(acc, xa + (wave * S + i + u) * 128, nt * xrow,
-                                                   wq[u], sc, zc, u, KG - step * SG, one_scale,
-                                                   z0, a.scale_elem);
+              step_product<FMT, GM, RAG, P, NT, D, false>(
+                  acc, xa + (wave * S + i + u) * 128, nt * xrow, nullptr, wq[u], sc, zc, u,
+                  KG - step * SG, one_scale, z0, a.scale_elem);
             weights_request(u);
           }
           if (next_round(pw)) weight_rows();
@@ -603,6 +635,10 @@ k_w4(W4Args a, int tile, int run) {
 // read twice.  x (R, 2, K) in two parts.  Grid: x the columns, y the token.
 constexpr int kTokenWaves = 8;   // routes at once
 constexpr int kTokenPart = 2048; // K elements of a route in LDS at a time
+template <int FMT, int GM>
+constexpr int token_lds() {
+  return 2 * kTokenPart * 2 + (FMT == W4_INT ? kTokenPart / 128 * GM * 4 : 0);
+}
 
 template <int FMT, int GM, bool RAG>
 __global__ void __launch_bounds__(kTokenWaves * 64, 2)
@@ -613,13 +649,14 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
   const int lane = threadIdx.x & 63, wave = wave_id(), waves = blockDim.x / 64;
   const int n16 = lane & 15, g = lane >> 4;
   const int t = blockIdx.y, n = min((int)blockIdx.x * 16 + n16, a.N - 1);
-  uint16_t* xs = reinterpret_cast<uint16_t*>(smem) + (size_t)wave * P * xrow;
+  uint16_t* xs = reinterpret_cast<uint16_t*>(smem + (size_t)wave * token_lds<FMT, GM>());
+  float* sums = reinterpret_cast<float*>(xs + P * xrow);  // of the scale groups
   const int KS = (a.K + 127) / 128, KG = a.K / a.group;
   const uint32_t pitch = (uint32_t)a.K / 2;
   const bool has_zero = FMT == W4_INT && a.zero;
   const float z0 = has_zero ? 128.f : 136.f;
   const bool one_scale = GM == 1 && FMT == W4_INT && KG == 1;
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;  // the product's rows all hold the token; the first is taken
 
   for (int q = wave; q < a.top_k; q += waves) {
     const int r = t * a.top_k + q;
@@ -667,7 +704,13 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
       }
 #pragma unroll
       for (int i = 0; i < kTokenPart / 512; ++i)
-        store_tokens<FMT, ELEM_PARTS>(xr[i], xs + i * 512 + lane * 8, xrow);
+      {
+        float v = store_tokens<FMT, ELEM_PARTS>(xr[i], xs + i * 512 + lane * 8, xrow);
+        if constexpr (FMT == W4_INT) {
+          v = group_sum<GM>(v);
+          if (lane % (16 / GM) == 0) sums[(i * 512 + lane * 8) / (128 / GM)] = v;
+        }
+      }
       __builtin_amdgcn_wave_barrier();  // the wave's own LDS, in order
       const int end = min(KS, (k0 + kTokenPart) / 128);
       for (int s0 = k0 / 128; s0 < end; s0 += D) {
@@ -681,20 +724,19 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
           if (s0 + u < KS)
-            step_product<FMT, GM, RAG, P, 1, D>(acc, xs + (s0 + u) * 128 - k0, xrow, wq[u], sc, zc,
-                                                u, KG - (s0 + u) * SG, one_scale, z0,
-                                                a.scale_elem);
+            step_product<FMT, GM, RAG, P, 1, D, true>(
+                acc, xs + (s0 + u) * 128 - k0, xrow, sums + ((s0 + u) - k0 / 128) * GM, wq[u], sc,
+                zc, u, KG - (s0 + u) * SG, one_scale, z0, a.scale_elem);
           weights_request(u, s0 + u + D);
         }
       }
       __builtin_amdgcn_wave_barrier();
     }
-    sum += weights[r] * acc[0];
+    sum += weights[r] * acc[0][0];
   }
-  // token rows: only the first of the product's 16 is one
   float* red = reinterpret_cast<float*>(smem);
   __syncthreads();  // the tokens are read
-  if (g == 0) red[wave * 16 + n16] = sum[0];
+  if (g == 0) red[wave * 16 + n16] = sum;
   __syncthreads();
   const int c = blockIdx.x * 16 + threadIdx.x;
   if (threadIdx.x < 16 && c < a.N) {
@@ -763,14 +805,17 @@ hipError_t launch_shape(const W4Args& a, int tile, hipStream_t stream) {
 template <int FMT, int XE, int GM, bool RAG>
 hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   // Tokens of one pass over the weights: 16, or 8 of two parts, so that two
-  // steps of them fit the LDS.  Where an expert has two routes or fewer on
-  // average, passes of half as many leave room for more steps ahead.
+  // steps of them fit the LDS.  Where the experts have few routes on average,
+  // passes of fewer tokens leave room for more steps ahead, and an expert with
+  // more routes takes another pass (T = 32, 256 experts, top-6: 369 us with
+  // passes of 4, 392 with 8).
   const int tokens = a.R / a.top_k;
   int tile = kTile / parts<XE>();
-  if (a.ids && a.R <= 2 * (int64_t)a.E) tile /= 2;
+  if (a.ids && a.R <= a.E) tile = 4;
+  else if (a.ids && a.R <= 2 * (int64_t)a.E) tile /= 2;
   if (tokens < tile) tile = tokens;
-  const int rounds = ((a.K + kUnit - 1) / kUnit + 3) / 4;
-  const bool whole = (kTokenLds / (parts<XE>() * tile * 2) - kPad) / kUnit >= 4 * rounds;
+  const int steps = ((a.K + kUnit - 1) / kUnit + 3) / 4 * 4;
+  const bool whole = (kTokenLds / (parts<XE>() * tile * 2) - kPad) / kUnit >= steps;
   if (whole) return launch_shape<FMT, XE, GM, RAG, true>(a, tile, stream);
   return launch_shape<FMT, XE, GM, RAG, false>(a, tile, stream);
 }
@@ -804,31 +849,39 @@ hipError_t launch_w4(int format, const W4Args& args, hipStream_t stream) {
 
 namespace {
 
+template <int FMT, int GM, bool RAG>
+hipError_t launch_token(const W4Args& a, const float* weights, int T, hipStream_t stream) {
+  auto* kernel = k_w4_token<FMT, GM, RAG>;
+  // eight waves take a little over the default limit of 64 KiB
+  static const hipError_t limit = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+      kTokenWaves * token_lds<FMT, GM>());
+  if (limit != hipSuccess) return limit;
+  const int waves = a.top_k < kTokenWaves ? a.top_k : kTokenWaves;
+  constexpr int lds = token_lds<FMT, GM>();
+  hipLaunchKernelGGL(kernel, dim3((a.N + 15) / 16, T), dim3(waves * 64), waves * lds, stream, a,
+                     weights);
+  return hipGetLastError();
+}
+
 template <int FMT, int GM>
-void launch_token(const W4Args& a, const float* weights, bool ragged, dim3 grid, int waves,
-                  size_t lds, hipStream_t stream) {
-  if (ragged)
-    hipLaunchKernelGGL((k_w4_token<FMT, GM, true>), grid, dim3(waves * 64), lds, stream, a, weights);
-  else
-    hipLaunchKernelGGL((k_w4_token<FMT, GM, false>), grid, dim3(waves * 64), lds, stream, a, weights);
+hipError_t launch_token(const W4Args& a, const float* weights, int T, hipStream_t stream) {
+  return a.K % 512 || a.group == a.K ? launch_token<FMT, GM, true>(a, weights, T, stream)
+                                     : launch_token<FMT, GM, false>(a, weights, T, stream);
 }
 
 }  // namespace
 
 hipError_t launch_w4_down(int format, const W4Args& a, const float* weights, float* y, int T,
                           hipStream_t stream) {
-  // One token's routes seldom share an expert, so its weights are read once
-  // either way.
+  // Few tokens' routes seldom share an expert, so its weights are read once
+  // either way (mx, 256 experts, top-6: 40.0 us against 44.0 for two tokens, 75
+  // against 75 for four; 8 experts, top-2, four tokens: 23.8 against 28.2).
   if (T <= kW4TokenMax) {
-    const int waves = a.top_k < kTokenWaves ? a.top_k : kTokenWaves;
-    const size_t lds = (size_t)waves * 2 * kTokenPart * 2;  // at most 64 KiB
-    const dim3 grid((a.N + 15) / 16, T);
-    const bool ragged = a.K % 512 || a.group == a.K;
-    if (format == W4_MX) launch_token<W4_MX, 1>(a, weights, ragged, grid, waves, lds, stream);
-    else if (a.group == 32) launch_token<W4_INT, 4>(a, weights, ragged, grid, waves, lds, stream);
-    else if (a.group == 64) launch_token<W4_INT, 2>(a, weights, ragged, grid, waves, lds, stream);
-    else launch_token<W4_INT, 1>(a, weights, ragged, grid, waves, lds, stream);
-    return hipGetLastError();
+    if (format == W4_MX) return launch_token<W4_MX, 1>(a, weights, T, stream);
+    if (a.group == 32) return launch_token<W4_INT, 4>(a, weights, T, stream);
+    if (a.group == 64) return launch_token<W4_INT, 2>(a, weights, T, stream);
+    return launch_token<W4_INT, 1>(a, weights, T, stream);
   }
   W4Args down = a;
   down.out = y;
