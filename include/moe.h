@@ -564,7 +564,7 @@ int fused_moe_down_combine(int32_t dtype, const void* w2, const void* w2_scale,
  * rounding at the end (no atomics): the same inputs give the same bits.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T < 0, K < 1, top_k < 1, n_shared < 0,
  * rows_cap outside [0, 2^31), T*(top_k + n_shared) >= 2^31),
- * MOE_ERR_UNSUPPORTED (elem; T * (K / 1024 + 1) or T * (top_k + n_shared),
+ * MOE_ERR_UNSUPPORTED (elem; T * (K / 1024 + 2) or T * (top_k + n_shared),
  * plus rows_cap / 4, past 2^24), MOE_ERR_ALIGN, MOE_ERR_HIP.
  */
 typedef enum {

@@ -513,15 +513,15 @@ _ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.uint8: 3, 
 
 def _operand(t, name, dtype, shape, dev):
     """Checks a dense tensor argument of the operators below; returns its address."""
-    if t.dtype is not dtype and t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype != dtype:
         raise MoeError(-3, f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise MoeError(-2, f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if t.device != dev:
         raise MoeError(-2, f"{name} must be on {dev} (got {t.device})")
-    if not t.is_contiguous():
-        raise MoeError(-2, f"{name} must be contiguous")
-    return t.data_ptr()
+    raise MoeError(-2, f"{name} must be contiguous")
 
 
 def _elem(t, name):

@@ -28,9 +28,9 @@ int check_rows(int32_t elem, int64_t T, int64_t K, int32_t top_k, int32_t n_shar
   if (rows_cap < 0 || rows_cap >= (int64_t(1) << 31))
     return abi_fail(MOE_ERR_SHAPE, "rows_cap must be in [0, 2^31) (got %lld)", (long long)rows_cap);
   if (K >= (int64_t(1) << 31)) return abi_fail(MOE_ERR_UNSUPPORTED, "K must be < 2^31");
-  // the launch's workgroups: at most one per 4,096 bytes of a token (or per
+  // the launch's workgroups: about one per 4,096 bytes of a token (or per
   // route), and one per four plan rows
-  const int64_t cols = K / 1024 + 1;
+  const int64_t cols = K / 1024 + 2;
   if (T * (cols > per ? cols : per) + rows_cap / 4 + 1 > kMaxGroups)
     return abi_fail(MOE_ERR_UNSUPPORTED, "T * K is too large for one launch");
   return MOE_OK;

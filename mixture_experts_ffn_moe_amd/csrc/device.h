@@ -244,6 +244,26 @@ __device__ __forceinline__ float max_dpp(float v) {
   return __builtin_fmaxf(v, __int_as_float(u));
 }
 
+// v plus the value lane movement CTRL (a DPP control) brings in
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+
+// sum over the wave, in every lane: each 16-lane row by lane movements, then the
+// four rows' sums read out; no LDS traffic
+__device__ __forceinline__ float wave_sum(float v) {
+  v = add_dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+  v = add_dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+  v = add_dpp<0x124>(v);  // row_ror 4
+  v = add_dpp<0x128>(v);  // row_ror 8
+  const int i = __float_as_int(v);
+  return (__int_as_float(__builtin_amdgcn_readlane(i, 0)) +
+          __int_as_float(__builtin_amdgcn_readlane(i, 16))) +
+         (__int_as_float(__builtin_amdgcn_readlane(i, 32)) +
+          __int_as_float(__builtin_amdgcn_readlane(i, 48)));
+}
+
 __device__ __forceinline__ float wave_max16(float v) {
   // max over the 16 lanes sharing l / 16, which form one DPP row: swap
   // neighbours, then pairs (each quad holds its max), then rotate the row

@@ -14,6 +14,8 @@
 // the same place, so no atomics and the same bits on every run.  Walking the
 // rows instead would read x top_k times.  Sums are fp32 in route order with
 // one rounding at the end.
+#include <type_traits>
+
 #include "device.h"
 #include "ops.h"
 
@@ -151,7 +153,9 @@ k_route_rows(const int32_t* __restrict__ ids, RowsArgs a, int E, int32_t* __rest
 
 // Workgroups [0, T * CB): the token blockIdx / CB, kThreads vectors of its
 // columns; then one for each kPadRows rows of the plan.
-template <int A>
+// A token's row is n16 whole vectors and the elements behind them: thread c of
+// the row has vector c, or element c - n16 of the rest.
+template <int ES, int A>
 __global__ void __launch_bounds__(kThreads)
 k_permute(RowsArgs a, const uint8_t* __restrict__ x, uint8_t* __restrict__ rows, int64_t pitch,
           int CB) {
@@ -169,12 +173,15 @@ k_permute(RowsArgs a, const uint8_t* __restrict__ x, uint8_t* __restrict__ rows,
       const int64_t p = row_of(a, route_of(a, t, j));
       if (p >= 0) store_vec<A>(rows + p * pitch + 16 * c, v);
     }
-  } else if (c == n16) {  // the bytes behind the last whole vector
-    for (int64_t e = 16 * n16; e < pitch; ++e)
-      for (int j = 0; j < nr; ++j) {
-        const int64_t p = row_of(a, route_of(a, t, j));
-        if (p >= 0) rows[p * pitch + e] = x[t * pitch + e];
-      }
+  } else if (A < 16 && c - n16 < pitch % 16 / ES) {
+    typedef typename std::conditional<ES == 4, uint32_t, typename std::conditional<ES == 2, uint16_t,
+                                                                          uint8_t>::type>::type unit;
+    const int64_t at = 16 * n16 + (c - n16) * ES;
+    const unit v = *reinterpret_cast<const unit*>(x + t * pitch + at);
+    for (int j = 0; j < nr; ++j) {
+      const int64_t p = row_of(a, route_of(a, t, j));
+      if (p >= 0) *reinterpret_cast<unit*>(rows + p * pitch + at) = v;
+    }
   }
 }
 
@@ -216,22 +223,27 @@ k_unpermute(RowsArgs a, const uint8_t* __restrict__ rows, uint8_t* __restrict__ 
       }
     }
     store_vec<A>(out + t * pitch + 16 * c, pack<ELEM>(s));
-  } else if (c == n16) {
-    for (int64_t e = n16 * V; e < a.K; ++e) {
-      float s = 0.f;
-      for (int j = 0; j < nr; ++j) {
-        const int64_t r = route_of(a, t, j), p = row_of(a, r);
-        if (p >= 0) s += weight_of(a, r, j) * load_elem<ELEM>(rows + p * pitch + e * ES);
-      }
-      store_elem<ELEM>(out + t * pitch + e * ES, s);
-    }
-  }
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
+  } else if (A < 16 && c - n16 < a.K % V) {  // an element behind the whole vectors
+    const int64_t at = (n16 * V + (c - n16)) * ES;
+    float s = 0.f;
+    for (int j0 = 0; j0 < nr; j0 += kBatch) {
+      float y[kBatch], w[kBatch];
 #pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+      for (int u = 0; u < kBatch; ++u) {
+        y[u] = w[u] = 0.f;
+        if (j0 + u < nr) {
+          const int64_t r = route_of(a, t, j0 + u), p = row_of(a, r);
+          if (p >= 0) {
+            w[u] = weight_of(a, r, j0 + u);
+            y[u] = load_elem<ELEM>(rows + p * pitch + at);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) s += w[u] * y[u];
+    }
+    store_elem<ELEM>(out + t * pitch + at, s);
+  }
 }
 
 // Workgroups [0, T * JG): token blockIdx / JG, its JB routes from
@@ -300,12 +312,13 @@ k_unpermute_backward(RowsArgs a, const uint8_t* __restrict__ d_out,
     __shared__ float part[kW][JB];
 #pragma unroll
     for (int u = 0; u < JB; ++u) {
+      if (j0 + u >= a.top_k) break;  // shared routes have no weight of their own
       const float s = wave_sum(dot[u]);
       if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][u] = s;
     }
     __syncthreads();
     const int u = threadIdx.x;
-    if (u < JB && j0 + u < a.top_k) {  // shared routes have no weight of their own
+    if (u < JB && j0 + u < a.top_k) {
       float s = 0.f;
       for (int v = 0; v < kW; ++v) s += part[v][u];
       d_w[t * a.top_k + j0 + u] = s;
@@ -337,6 +350,15 @@ k_route_backward(const int32_t* __restrict__ ids, const float* __restrict__ w,
   }
   const float mean = wave_sum(wj * gj);
   const float d = wj * (gj - mean);
+  // every route's id and term as wave-uniform values, read while all lanes are
+  // active: in the loop below a lane that holds one may not be
+  int ij[kMaxTopK];
+  float dj[kMaxTopK];
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+    ij[j] = __builtin_amdgcn_readlane(id, j);
+    dj[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
+  }
   float* row = d_logits + t * E;
   constexpr int V = A / 4;
   for (int e = lane * V; e < E; e += 64 * V) {
@@ -346,11 +368,9 @@ k_route_backward(const int32_t* __restrict__ ids, const float* __restrict__ w,
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j) {
       if (j >= top_k) break;
-      const int ij = __builtin_amdgcn_readlane(id, j);
-      const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (e + v == ij) s[v] += dj;
+        if (e + v == ij[j]) s[v] += dj[j];
     }
     if constexpr (V == 4) *reinterpret_cast<float4*>(row + e) = make_float4(s[0], s[1], s[2], s[3]);
     else row[e] = s[0];
@@ -365,8 +385,9 @@ hipError_t by_pitch(int64_t pitch, F16 aligned, FE other) {
   return hipGetLastError();
 }
 
-int col_blocks(int64_t pitch) {
-  return (int)((pitch / 16 + (pitch % 16 ? 1 : 0) + kThreads - 1) / kThreads);
+// workgroups of a token's row: its vectors and the elements behind them
+int col_blocks(int64_t pitch, int es) {
+  return (int)((pitch / 16 + pitch % 16 / es + kThreads - 1) / kThreads);
 }
 
 template <int ELEM, int A, int JB>
@@ -399,19 +420,19 @@ hipError_t launch_route_rows(const int32_t* ids, const RowsArgs& a, int E, int32
 hipError_t launch_permute(int elem, const RowsArgs& a, const void* x, void* rows,
                           hipStream_t stream) {
   const int64_t pitch = a.K * elem_bytes(elem);
-  const int CB = col_blocks(pitch);
+  const int CB = col_blocks(pitch, elem_bytes(elem));
   const dim3 grid((unsigned)(a.T * CB + (a.cap + kPadRows - 1) / kPadRows));
   if (grid.x == 0) return hipSuccess;
   auto s = static_cast<const uint8_t*>(x);
   auto d = static_cast<uint8_t*>(rows);
-#define MOE_PERMUTE(A) \
-  hipLaunchKernelGGL(k_permute<A>, grid, dim3(kThreads), 0, stream, a, s, d, pitch, CB)
+#define MOE_PERMUTE(ES, A) \
+  hipLaunchKernelGGL((k_permute<ES, A>), grid, dim3(kThreads), 0, stream, a, s, d, pitch, CB)
   return by_pitch(
-      pitch, [&] { MOE_PERMUTE(16); },
+      pitch, [&] { MOE_PERMUTE(1, 16); },
       [&] {
-        if (elem == ELEM_F32) MOE_PERMUTE(4);
-        else if (elem == ELEM_U8) MOE_PERMUTE(1);
-        else MOE_PERMUTE(2);
+        if (elem == ELEM_F32) MOE_PERMUTE(4, 4);
+        else if (elem == ELEM_U8) MOE_PERMUTE(1, 1);
+        else MOE_PERMUTE(2, 2);
       });
 #undef MOE_PERMUTE
 }
@@ -419,7 +440,7 @@ hipError_t launch_permute(int elem, const RowsArgs& a, const void* x, void* rows
 hipError_t launch_unpermute(int elem, const RowsArgs& a, const void* rows, void* out,
                             hipStream_t stream) {
   const int64_t pitch = a.K * elem_bytes(elem);
-  const int CB = col_blocks(pitch);
+  const int CB = col_blocks(pitch, elem_bytes(elem));
   const dim3 grid((unsigned)(a.T * CB));
   if (grid.x == 0) return hipSuccess;
   auto y = static_cast<const uint8_t*>(rows);

@@ -124,12 +124,6 @@ __device__ __forceinline__ int place_of(int i) {
 __device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return (a & 0xFFFFu) | b << 16; }
 __device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return a >> 16 | (b & 0xFFFF0000u); }
 
-// v and what lane movement CTRL brings in, added
-template <int CTRL>
-__device__ __forceinline__ float add_dpp(float v) {
-  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
-}
-
 // Lanes of a 16-lane row that hold one scale group's 8-element shares (GM groups
 // in the row's 128 elements): every lane gets their sum.
 template <int GM>
