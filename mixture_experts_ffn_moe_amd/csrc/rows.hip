@@ -328,18 +328,22 @@ k_unpermute_backward(RowsArgs a, const uint8_t* __restrict__ d_out,
 
 // d_logits[t, e] = sum over j with ids[t, j] = e of w_j (dw_j - <w, dw>): the
 // gradient of a softmax over the selected logits, which is what the
-// normalized routing weights are.  One wave a token; lane j < top_k holds
-// route j.  Every element is written once, so an id that occurs twice needs no
-// atomics; 4 T E bytes of output bound it.
+// normalized routing weights are.  4 T E bytes of output bound it.  One wave a
+// token; lane j < top_k holds route j and adds the terms of the routes with its
+// id in their order, so that an id that occurs twice needs no atomics.  The row
+// is put together in LDS: comparing every output with every route's id instead
+// made the vector units the bound (8,192 tokens, 288 experts, top-8: 8.0 us).
 constexpr int kMaxTopK = 16;
+constexpr int kMaxExperts = 1024;
 
 template <int A>
 __global__ void __launch_bounds__(kThreads)
 k_route_backward(const int32_t* __restrict__ ids, const float* __restrict__ w,
                  const float* __restrict__ dw, float* __restrict__ d_logits, int64_t T, int E,
                  int top_k) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wave_id();
+  __shared__ __align__(16) float lds[kThreads / 64][kMaxExperts];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wave;
   if (t >= T) return;
   int id = -1;
   float wj = 0.f, gj = 0.f;
@@ -348,32 +352,29 @@ k_route_backward(const int32_t* __restrict__ ids, const float* __restrict__ w,
     wj = w[t * top_k + lane];
     gj = dw[t * top_k + lane];
   }
+  float* line = lds[wave];  // the wave's own: its LDS operations stay in order
+  for (int e = lane * 4; e < E; e += 256)
+    *reinterpret_cast<float4*>(line + e) = make_float4(0.f, 0.f, 0.f, 0.f);
   const float mean = wave_sum(wj * gj);
   const float d = wj * (gj - mean);
-  // every route's id and term as wave-uniform values, read while all lanes are
-  // active: in the loop below a lane that holds one may not be
-  int ij[kMaxTopK];
-  float dj[kMaxTopK];
+  float s = 0.f;
 #pragma unroll
   for (int j = 0; j < kMaxTopK; ++j) {
-    ij[j] = __builtin_amdgcn_readlane(id, j);
-    dj[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
+    if (j >= top_k) break;
+    const int ij = __builtin_amdgcn_readlane(id, j);
+    const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
+    if (id == ij) s += dj;
   }
+  __builtin_amdgcn_wave_barrier();
+  if (lane < top_k && (unsigned)id < (unsigned)E) line[id] = s;
+  __builtin_amdgcn_wave_barrier();
   float* row = d_logits + t * E;
   constexpr int V = A / 4;
   for (int e = lane * V; e < E; e += 64 * V) {
-    float s[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = 0.f;
-#pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= top_k) break;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e + v == ij[j]) s[v] += dj[j];
-    }
-    if constexpr (V == 4) *reinterpret_cast<float4*>(row + e) = make_float4(s[0], s[1], s[2], s[3]);
-    else row[e] = s[0];
+    if constexpr (V == 4)
+      *reinterpret_cast<float4*>(row + e) = *reinterpret_cast<const float4*>(line + e);
+    else
+      row[e] = line[e];
   }
 }
 
