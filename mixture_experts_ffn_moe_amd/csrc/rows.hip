@@ -47,14 +47,19 @@ struct VecOf<1> {
   typedef vec_a type __attribute__((aligned(1)));
 };
 
-template <int A>
+// STREAM: past the caches, for rows that would only push each other out of them.
+template <int A, bool STREAM = false>
 __device__ __forceinline__ vec_a load_vec(const uint8_t* p) {
-  return *reinterpret_cast<const typename VecOf<A>::type*>(p);
+  auto q = reinterpret_cast<const typename VecOf<A>::type*>(p);
+  if constexpr (STREAM) return __builtin_nontemporal_load(q);
+  return *q;
 }
 
-template <int A>
+template <int A, bool STREAM = false>
 __device__ __forceinline__ void store_vec(uint8_t* p, vec_a v) {
-  *reinterpret_cast<typename VecOf<A>::type*>(p) = v;
+  auto q = reinterpret_cast<typename VecOf<A>::type*>(p);
+  if constexpr (STREAM) __builtin_nontemporal_store(v, q);
+  else *q = v;
 }
 
 template <int ELEM>
@@ -123,7 +128,7 @@ __device__ __forceinline__ float weight_of(const RowsArgs& a, int64_t r, int j) 
 }
 
 // Zeroes the plan's padding rows among kPadRows rows from p0.
-template <int A>
+template <int A, bool STREAM>
 __device__ __forceinline__ void zero_padding(const RowsArgs& a, int64_t p0, uint8_t* rows,
                                              int64_t pitch) {
   const int64_t used = min((int64_t)*a.ntp, a.cap);
@@ -133,7 +138,8 @@ __device__ __forceinline__ void zero_padding(const RowsArgs& a, int64_t p0, uint
     if (a.sorted[p] >= 0) continue;
     uint8_t* d = rows + p * pitch;
     const int64_t n16 = pitch / 16;
-    for (int64_t c = threadIdx.x; c < n16; c += kThreads) store_vec<A>(d + 16 * c, vec_a{0, 0, 0, 0});
+    for (int64_t c = threadIdx.x; c < n16; c += kThreads)
+      store_vec<A, STREAM>(d + 16 * c, vec_a{0, 0, 0, 0});
     for (int64_t b = 16 * n16 + threadIdx.x; b < pitch; b += kThreads) d[b] = 0;
   }
 }
@@ -155,13 +161,13 @@ k_route_rows(const int32_t* __restrict__ ids, RowsArgs a, int E, int32_t* __rest
 // columns; then one for each kPadRows rows of the plan.
 // A token's row is n16 whole vectors and the elements behind them: thread c of
 // the row has vector c, or element c - n16 of the rest.
-template <int ES, int A>
+template <int ES, int A, bool STREAM>
 __global__ void __launch_bounds__(kThreads)
 k_permute(RowsArgs a, const uint8_t* __restrict__ x, uint8_t* __restrict__ rows, int64_t pitch,
           int CB) {
   const int64_t b = blockIdx.x;
   if (b >= a.T * CB) {
-    zero_padding<A>(a, (b - a.T * CB) * kPadRows, rows, pitch);
+    zero_padding<A, STREAM>(a, (b - a.T * CB) * kPadRows, rows, pitch);
     return;
   }
   const int64_t t = b / CB;
@@ -171,7 +177,7 @@ k_permute(RowsArgs a, const uint8_t* __restrict__ x, uint8_t* __restrict__ rows,
     const vec_a v = load_vec<A>(x + t * pitch + 16 * c);
     for (int j = 0; j < nr; ++j) {
       const int64_t p = row_of(a, route_of(a, t, j));
-      if (p >= 0) store_vec<A>(rows + p * pitch + 16 * c, v);
+      if (p >= 0) store_vec<A, STREAM>(rows + p * pitch + 16 * c, v);
     }
   } else if (A < 16 && c - n16 < pitch % 16 / ES) {
     typedef typename std::conditional<ES == 4, uint32_t, typename std::conditional<ES == 2, uint16_t,
@@ -185,7 +191,7 @@ k_permute(RowsArgs a, const uint8_t* __restrict__ x, uint8_t* __restrict__ rows,
   }
 }
 
-template <int ELEM, int A>
+template <int ELEM, int A, bool STREAM>
 __global__ void __launch_bounds__(kThreads)
 k_unpermute(RowsArgs a, const uint8_t* __restrict__ rows, uint8_t* __restrict__ out, int CB) {
   constexpr int V = per_vec<ELEM>(), ES = elem_bytes(ELEM), kBatch = 8;
@@ -209,7 +215,7 @@ k_unpermute(RowsArgs a, const uint8_t* __restrict__ rows, uint8_t* __restrict__ 
           if (p >= 0) {
             placed[u] = true;
             w[u] = weight_of(a, r, j0 + u);
-            y[u] = load_vec<A>(rows + p * pitch + 16 * c);
+            y[u] = load_vec<A, STREAM>(rows + p * pitch + 16 * c);
           }
         }
       }
@@ -249,7 +255,7 @@ k_unpermute(RowsArgs a, const uint8_t* __restrict__ rows, uint8_t* __restrict__ 
 // Workgroups [0, T * JG): token blockIdx / JG, its JB routes from
 // (blockIdx % JG) * JB; then one for each kPadRows rows of the plan.
 // With DW the dot products too.
-template <int ELEM, int A, int JB, bool DW>
+template <int ELEM, int A, int JB, bool DW, bool STREAM>
 __global__ void __launch_bounds__(kThreads)
 k_unpermute_backward(RowsArgs a, const uint8_t* __restrict__ d_out,
                      const uint8_t* __restrict__ rows, uint8_t* __restrict__ d_rows,
@@ -257,7 +263,7 @@ k_unpermute_backward(RowsArgs a, const uint8_t* __restrict__ d_out,
   constexpr int V = per_vec<ELEM>(), ES = elem_bytes(ELEM), kW = kThreads / 64;
   const int64_t pitch = a.K * ES, n16 = pitch / 16, b = blockIdx.x;
   if (b >= a.T * JG) {
-    zero_padding<A>(a, (b - a.T * JG) * kPadRows, d_rows, pitch);
+    zero_padding<A, STREAM>(a, (b - a.T * JG) * kPadRows, d_rows, pitch);
     return;
   }
   const int64_t t = b / JG;
@@ -280,7 +286,7 @@ k_unpermute_backward(RowsArgs a, const uint8_t* __restrict__ d_out,
     if constexpr (DW) {
 #pragma unroll
       for (int u = 0; u < JB; ++u)
-        if (p[u] >= 0) y[u] = load_vec<A>(rows + p[u] * pitch + 16 * c);
+        if (p[u] >= 0) y[u] = load_vec<A, STREAM>(rows + p[u] * pitch + 16 * c);
     }
     float f[V];
     unpack<ELEM>(g, f);
@@ -290,7 +296,7 @@ k_unpermute_backward(RowsArgs a, const uint8_t* __restrict__ d_out,
       float d[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) d[e] = w[u] * f[e];
-      store_vec<A>(d_rows + p[u] * pitch + 16 * c, pack<ELEM>(d));
+      store_vec<A, STREAM>(d_rows + p[u] * pitch + 16 * c, pack<ELEM>(d));
       if constexpr (DW) {
         float h[V];
         unpack<ELEM>(y[u], h);
@@ -378,12 +384,13 @@ k_route_backward(const int32_t* __restrict__ ids, const float* __restrict__ w,
   }
 }
 
-// alignment of a row's vectors: 16 bytes where the pitch keeps it, else the element's
-template <class F16, class FE>
-hipError_t by_pitch(int64_t pitch, F16 aligned, FE other) {
-  if (pitch % 16 == 0) aligned();
-  else other();
-  return hipGetLastError();
+// Whether the routes' rows are streamed past the caches: once they outgrow the
+// 256 MiB memory-side cache.  Measured at K = 4096, top-8 (permute, then
+// unpermute): 8,192 tokens (537 MB) 220 us streamed against 262, 4,096 tokens
+// 113 against 134; 2,048 tokens (134 MB), whose rows the second call finds in the
+// cache, 61 against 56, and 64 tokens 29 against 23.
+bool streams(const RowsArgs& a, int64_t pitch) {
+  return a.T * (a.top_k + a.n_shared) * pitch > (int64_t(192) << 20);
 }
 
 // workgroups of a token's row: its vectors and the elements behind them
@@ -391,20 +398,59 @@ int col_blocks(int64_t pitch, int es) {
   return (int)((pitch / 16 + pitch % 16 / es + kThreads - 1) / kThreads);
 }
 
-template <int ELEM, int A, int JB>
-void backward_grid(const RowsArgs& a, const void* d_out, const void* rows, void* d_rows,
-                   float* d_w, hipStream_t stream) {
+// Runs f<alignment of a row's vectors, STREAM>: 16 bytes where the pitch keeps
+// it, else the element's (A < 16, never streamed: such rows are short of the
+// bandwidth where that matters).
+template <int ES, class F>
+hipError_t by_pitch(const RowsArgs& a, int64_t pitch, F f) {
+  typedef std::integral_constant<int, 16> whole;
+  typedef std::integral_constant<int, ES> element;
+  if (pitch % 16) f(element{}, std::false_type{});
+  else if (streams(a, pitch)) f(whole{}, std::true_type{});
+  else f(whole{}, std::false_type{});
+  return hipGetLastError();
+}
+
+template <int ELEM, int A, bool STREAM>
+void unpermute_backward(const RowsArgs& a, const void* d_out, const void* rows, void* d_rows,
+                        float* d_w, hipStream_t stream) {
+  constexpr int JB = 8;
   const int JG = (a.top_k + a.n_shared + JB - 1) / JB;
   const dim3 grid((unsigned)(a.T * JG + (a.cap + kPadRows - 1) / kPadRows));
   auto g = static_cast<const uint8_t*>(d_out);
   auto y = static_cast<const uint8_t*>(rows);
   auto d = static_cast<uint8_t*>(d_rows);
   if (d_w)
-    hipLaunchKernelGGL((k_unpermute_backward<ELEM, A, JB, true>), grid, dim3(kThreads), 0, stream,
-                       a, g, y, d, d_w, JG);
+    hipLaunchKernelGGL((k_unpermute_backward<ELEM, A, JB, true, STREAM>), grid, dim3(kThreads), 0,
+                       stream, a, g, y, d, d_w, JG);
   else
-    hipLaunchKernelGGL((k_unpermute_backward<ELEM, A, JB, false>), grid, dim3(kThreads), 0, stream,
-                       a, g, y, d, d_w, JG);
+    hipLaunchKernelGGL((k_unpermute_backward<ELEM, A, JB, false, STREAM>), grid, dim3(kThreads), 0,
+                       stream, a, g, y, d, d_w, JG);
+}
+
+template <int ES>
+hipError_t permute(const RowsArgs& a, const void* x, void* rows, hipStream_t stream) {
+  const int64_t pitch = a.K * ES;
+  const int CB = col_blocks(pitch, ES);
+  const dim3 grid((unsigned)(a.T * CB + (a.cap + kPadRows - 1) / kPadRows));
+  if (grid.x == 0) return hipSuccess;
+  return by_pitch<ES>(a, pitch, [&](auto A, auto STREAM) {
+    hipLaunchKernelGGL((k_permute<ES, A(), STREAM()>), grid, dim3(kThreads), 0, stream, a,
+                       static_cast<const uint8_t*>(x), static_cast<uint8_t*>(rows), pitch, CB);
+  });
+}
+
+template <int ELEM>
+hipError_t unpermute(const RowsArgs& a, const void* rows, void* out, hipStream_t stream) {
+  constexpr int ES = elem_bytes(ELEM);
+  const int64_t pitch = a.K * ES;
+  const int CB = col_blocks(pitch, ES);
+  const dim3 grid((unsigned)(a.T * CB));
+  if (grid.x == 0) return hipSuccess;
+  return by_pitch<ES>(a, pitch, [&](auto A, auto STREAM) {
+    hipLaunchKernelGGL((k_unpermute<ELEM, A(), STREAM()>), grid, dim3(kThreads), 0, stream, a,
+                       static_cast<const uint8_t*>(rows), static_cast<uint8_t*>(out), CB);
+  });
 }
 
 }  // namespace
@@ -420,65 +466,31 @@ hipError_t launch_route_rows(const int32_t* ids, const RowsArgs& a, int E, int32
 
 hipError_t launch_permute(int elem, const RowsArgs& a, const void* x, void* rows,
                           hipStream_t stream) {
-  const int64_t pitch = a.K * elem_bytes(elem);
-  const int CB = col_blocks(pitch, elem_bytes(elem));
-  const dim3 grid((unsigned)(a.T * CB + (a.cap + kPadRows - 1) / kPadRows));
-  if (grid.x == 0) return hipSuccess;
-  auto s = static_cast<const uint8_t*>(x);
-  auto d = static_cast<uint8_t*>(rows);
-#define MOE_PERMUTE(ES, A) \
-  hipLaunchKernelGGL((k_permute<ES, A>), grid, dim3(kThreads), 0, stream, a, s, d, pitch, CB)
-  return by_pitch(
-      pitch, [&] { MOE_PERMUTE(1, 16); },
-      [&] {
-        if (elem == ELEM_F32) MOE_PERMUTE(4, 4);
-        else if (elem == ELEM_U8) MOE_PERMUTE(1, 1);
-        else MOE_PERMUTE(2, 2);
-      });
-#undef MOE_PERMUTE
+  if (elem == ELEM_F32) return permute<4>(a, x, rows, stream);
+  if (elem == ELEM_U8) return permute<1>(a, x, rows, stream);
+  return permute<2>(a, x, rows, stream);
 }
 
 hipError_t launch_unpermute(int elem, const RowsArgs& a, const void* rows, void* out,
                             hipStream_t stream) {
-  const int64_t pitch = a.K * elem_bytes(elem);
-  const int CB = col_blocks(pitch, elem_bytes(elem));
-  const dim3 grid((unsigned)(a.T * CB));
-  if (grid.x == 0) return hipSuccess;
-  auto y = static_cast<const uint8_t*>(rows);
-  auto o = static_cast<uint8_t*>(out);
-#define MOE_UNPERMUTE(ELEM, A) \
-  hipLaunchKernelGGL((k_unpermute<ELEM, A>), grid, dim3(kThreads), 0, stream, a, y, o, CB)
-  return by_pitch(
-      pitch,
-      [&] {
-        if (elem == ELEM_F32) MOE_UNPERMUTE(ELEM_F32, 16);
-        else if (elem == ELEM_F16) MOE_UNPERMUTE(ELEM_F16, 16);
-        else MOE_UNPERMUTE(ELEM_BF16, 16);
-      },
-      [&] {
-        if (elem == ELEM_F32) MOE_UNPERMUTE(ELEM_F32, 4);
-        else if (elem == ELEM_F16) MOE_UNPERMUTE(ELEM_F16, 2);
-        else MOE_UNPERMUTE(ELEM_BF16, 2);
-      });
-#undef MOE_UNPERMUTE
+  if (elem == ELEM_F32) return unpermute<ELEM_F32>(a, rows, out, stream);
+  if (elem == ELEM_F16) return unpermute<ELEM_F16>(a, rows, out, stream);
+  return unpermute<ELEM_BF16>(a, rows, out, stream);
 }
 
 hipError_t launch_unpermute_backward(int elem, const RowsArgs& a, const void* d_out,
                                      const void* rows, void* d_rows, float* d_w,
                                      hipStream_t stream) {
   if (a.T == 0 && a.cap == 0) return hipSuccess;
-  return by_pitch(
-      a.K * elem_bytes(elem),
-      [&] {
-        if (elem == ELEM_F32) backward_grid<ELEM_F32, 16, 8>(a, d_out, rows, d_rows, d_w, stream);
-        else if (elem == ELEM_F16) backward_grid<ELEM_F16, 16, 8>(a, d_out, rows, d_rows, d_w, stream);
-        else backward_grid<ELEM_BF16, 16, 8>(a, d_out, rows, d_rows, d_w, stream);
-      },
-      [&] {
-        if (elem == ELEM_F32) backward_grid<ELEM_F32, 4, 8>(a, d_out, rows, d_rows, d_w, stream);
-        else if (elem == ELEM_F16) backward_grid<ELEM_F16, 2, 8>(a, d_out, rows, d_rows, d_w, stream);
-        else backward_grid<ELEM_BF16, 2, 8>(a, d_out, rows, d_rows, d_w, stream);
-      });
+  auto run = [&](auto ELEM) {
+    constexpr int ES = elem_bytes(ELEM());
+    return by_pitch<ES>(a, a.K * ES, [&](auto A, auto STREAM) {
+      unpermute_backward<ELEM(), A(), STREAM()>(a, d_out, rows, d_rows, d_w, stream);
+    });
+  };
+  if (elem == ELEM_F32) return run(std::integral_constant<int, ELEM_F32>{});
+  if (elem == ELEM_F16) return run(std::integral_constant<int, ELEM_F16>{});
+  return run(std::integral_constant<int, ELEM_BF16>{});
 }
 
 hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw,
