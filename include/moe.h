@@ -651,10 +651,11 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const
  *                    contraction is a multiple of it (of 128 for 0).
  *   topk_ids         (T, top_k) int32: expert of each route.  A route whose
  *                    id is outside [0, E) gives zeros.
- * Limits: T * top_k <= 4096 routes, N * K < 2^32.  An expert's weights are
- * read once for up to 16 of its routes (bf16; 8 for fp16 and in the second
- * product of fused_moe_w4).  Sums are fp32 in a fixed order: the same inputs
- * give the same bits.  An infinite activation gives NaN.
+ * Limits: T * top_k <= 4096 routes, N * K < 2^32.  The calls are made for few
+ * routes per expert: its weights are read again for every 16 of them at most
+ * (fewer where experts have few on average).  Sums are fp32 in a fixed order:
+ * the same inputs give the same bits.  An infinite activation gives NaN or an
+ * infinity.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_ALIGN,
  * MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 is a successful no-op.
  */
@@ -672,8 +673,8 @@ int moe_w4_matvec(int32_t format, int32_t elem, const void* x, int32_t x_per_rou
 
 /* The whole expert FFN: out[t] = sum_j topk_weights[t][j] * W2[e] . silu(gate)
  * * up, with gate, up = W1[e] . x[t], for the routes with e = topk_ids[t][j]
- * in [0, E); one rounding to elem at the end, the intermediate held in fp32
- * (and entering the second product as two bf16 parts).  w1 (E, N, K/2), w2
+ * in [0, E); one rounding to elem at the end, the intermediate held as two
+ * bf16 parts (16 significant bits).  w1 (E, N, K/2), w2
  * (E, K, N/4) bytes, N = 2I, with scales and zeros along K and I.  The
  * workspace (device, 16-byte aligned, contents undefined on return; separate
  * for calls that may overlap) has at least moe_w4_workspace_size bytes. */

@@ -537,6 +537,14 @@ def _on_gpu(t, name):
         raise MoeError(-2, f"{name} must be on a GPU (got {t.device})")
 
 
+def _matrix(t, name):
+    """The two sizes of a matrix argument."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise MoeError(-2, f"{name} must have two dimensions (got shape {tuple(shape)})")
+    return shape
+
+
 def _output(out, name, shape, dtype, dev, stream):
     """The caller's output, checked, or a new one of the stream the call runs on."""
     if out is not None:
@@ -579,7 +587,7 @@ def moe_route_rows(topk_ids, num_experts, sorted_token_ids, num_tokens_post_padd
     """The inverse of a plan: (T * (top_k + n_shared)) int32, the row of each
     route in the plan moe_align / moe_align_shared made of ``topk_ids``, -1
     for a route that has none.  One such map serves the four calls below."""
-    T, k = topk_ids.shape
+    T, k = _matrix(topk_ids, "topk_ids")
     dev = topk_ids.device
     _on_gpu(topk_ids, "topk_ids")
     cap = sorted_token_ids.numel()
@@ -598,7 +606,7 @@ def moe_permute(x, row_of_route, sorted_token_ids, num_tokens_post_padded, top_k
     routed token in its routes' rows, zeros in the padding rows.  Rows at or
     past num_tokens_post_padded are left as they are (unspecified in a new
     tensor).  x: bf16, fp16, fp32, or one-byte values (e4m3, scales)."""
-    T, K = x.shape
+    T, K = _matrix(x, "x")
     dev = x.device
     elem = _elem(x, "x")
     cap = sorted_token_ids.numel()
@@ -614,7 +622,7 @@ def moe_permute(x, row_of_route, sorted_token_ids, num_tokens_post_padded, top_k
 
 def moe_permute_backward(d_rows, row_of_route, top_k, n_shared=0, stream=None, out=None):
     """Gradient of moe_permute: each token's sum of its rows' gradients."""
-    cap, K = d_rows.shape
+    cap, K = _matrix(d_rows, "d_rows")
     dev = d_rows.device
     elem = _elem(d_rows, "d_rows")
     n = row_of_route.numel()
@@ -632,7 +640,7 @@ def moe_unpermute(rows, row_of_route, topk_weights, top_k, n_shared=0, stream=No
     routes of topk_weights[t, j] * row (weight 1 for shared routes, and for
     all of them without ``topk_weights``).  A token without rows gets zeros.
     ``row_of_route`` None: row r holds route r."""
-    cap, K = rows.shape
+    cap, K = _matrix(rows, "rows")
     dev = rows.device
     elem = _elem(rows, "rows")
     n = cap if row_of_route is None else row_of_route.numel()
@@ -655,7 +663,7 @@ def moe_unpermute_backward(d_out, rows, row_of_route, sorted_token_ids, num_toke
     num_tokens_post_padded are left as they are), the weights' (T, top_k)
     fp32.  ``rows`` None: only d_rows, and d_weights is None.  ``out`` may pass
     the two preallocated."""
-    T, K = d_out.shape
+    T, K = _matrix(d_out, "d_out")
     dev = d_out.device
     elem = _elem(d_out, "d_out")
     cap = sorted_token_ids.numel()
@@ -680,7 +688,7 @@ def moe_route_backward(topk_ids, topk_weights, d_weights, num_experts, stream=No
     """Gradient of moe_route_align's weights with respect to its logits,
     (T, num_experts) fp32, from topk_ids and topk_weights as it returned them
     and the weights' gradient."""
-    T, k = topk_ids.shape
+    T, k = _matrix(topk_ids, "topk_ids")
     dev = topk_ids.device
     _on_gpu(topk_ids, "topk_ids")
     ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
@@ -738,7 +746,7 @@ def moe_w4_matvec(fmt, x, w, w_scale, w_zero, topk_ids, group, swiglu=False, str
         xp = _operand(x, "x", x.dtype, (T, K), dev)
         shape = (T, n)
     else:
-        k = topk_ids.shape[1]
+        _, k = _matrix(topk_ids, "topk_ids")
         per_route = int(x.dim() == 3)
         xp = _operand(x, "x", x.dtype, (T, k, K) if per_route else (T, K), dev)
         ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
@@ -765,11 +773,11 @@ def fused_moe_w4(fmt, x, w1, w1_scale, w1_zero, w2, w2_scale, w2_zero, topk_ids,
     that every token routes to with weight 1."""
     f, elem = _w4_types(fmt, x)
     dev = x.device
-    if w1.dim() != 3 or x.dim() != 2 or topk_ids.dim() != 2:
-        raise MoeError(-2, "x must be (T, K), w1 (E, N, K/2) and topk_ids (T, top_k)")
+    if w1.dim() != 3:
+        raise MoeError(-2, f"w1 must have shape (E, N, K/2) (got {tuple(w1.shape)})")
     E, N, _ = w1.shape
-    T, K = x.shape
-    k = topk_ids.shape[1]
+    T, K = _matrix(x, "x")
+    _, k = _matrix(topk_ids, "topk_ids")
     xp = _operand(x, "x", x.dtype, (T, K), dev)
     p1 = _w4_weights(f, "w1", w1, w1_scale, w1_zero, E, N, K, group, x.dtype, dev)
     p2 = _w4_weights(f, "w2", w2, w2_scale, w2_zero, E, K, N // 2, group, x.dtype, dev)

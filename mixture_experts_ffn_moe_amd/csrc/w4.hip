@@ -38,6 +38,8 @@
 // LDS at the end.  The tokens' part of K lies in LDS, in the order
 // the weights need.  Where there are many tiles a workgroup takes several in a
 // row, requesting the next one's weights while it ends the last.
+#include <atomic>
+
 #include "device.h"
 #include "ops.h"
 
@@ -846,11 +848,20 @@ namespace {
 template <int FMT, int GM, bool RAG>
 hipError_t launch_token(const W4Args& a, const float* weights, int T, hipStream_t stream) {
   auto* kernel = k_w4_token<FMT, GM, RAG>;
-  // eight waves take a little over the default limit of 64 KiB
-  static const hipError_t limit = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-      kTokenWaves * token_lds<FMT, GM>());
-  if (limit != hipSuccess) return limit;
+  // eight waves take a little over the default limit of 64 KiB: raised once on
+  // each device
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev > 63 || !(raised.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize,
+                            kTokenWaves * token_lds<FMT, GM>());
+    if (e != hipSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
   const int waves = a.top_k < kTokenWaves ? a.top_k : kTokenWaves;
   constexpr int lds = token_lds<FMT, GM>();
   hipLaunchKernelGGL(kernel, dim3((a.N + 15) / 16, T), dim3(waves * 64), waves * lds, stream, a,
