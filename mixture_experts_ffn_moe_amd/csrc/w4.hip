@@ -69,13 +69,18 @@ __device__ __forceinline__ int buf_loadu16(__amdgpu_buffer_rsrc_t r, uint32_t vo
   return (int)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)voff, (int)soff, 0);
 }
 
+// The two constants of the int4 conversion, in registers: as literals the
+// compiler takes an and and an or for each pair where one v_and_or does.
+struct Int4Bits {
+  uint32_t mask = 0x000F000Fu, bias = 0x43004300u;
+  __device__ __forceinline__ Int4Bits() { asm("" : "+s"(mask), "+v"(bias)); }
+};
+
 // 8 int4 codes of one dword as bf16 128 + q, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8 int4_to_bf16(uint32_t v) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  u32x4 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = ((v >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-  return __builtin_bit_cast(bf16x8, o);
+__device__ __forceinline__ bf16x8 int4_to_bf16(uint32_t v, const Int4Bits& c) {
+  return __builtin_bit_cast(
+      bf16x8, make_uint4((v & c.mask) | c.bias, ((v >> 4) & c.mask) | c.bias,
+                         ((v >> 8) & c.mask) | c.bias, ((v >> 12) & c.mask) | c.bias));
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -237,14 +242,15 @@ using ScaleWindow = Window<D * step_scales<FMT, GM>() * scale_bytes<FMT>(), RAG>
 // xp: the lane's token at this step in LDS, the parts `part` elements apart.
 // valid: the scale groups of the step that the row has (RAG).  ONE: every row
 // of the product is the same token, whose sum over group q of the step is sx[q];
-// only the first row is made.
-template <int FMT, int GM, bool RAG, int P, int NT, int D, bool ONE>
+// only the first row is made.  SE: type of int4 scales.
+template <int FMT, int GM, bool RAG, int P, int NT, int D, bool ONE, int SE>
 __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* xp, int part,
                                              const float* sx,
                                              const uint4 (&wq)[NT],
                                              const ScaleWindow<FMT, D, GM, RAG> (&sc)[NT],
                                              const ZeroWindow<D, GM, RAG> (&zc)[NT], int u,
-                                             int valid, bool one_scale, float z0, int scale_elem) {
+                                             int valid, bool one_scale, float z0,
+                                             const Int4Bits& bits) {
   const int g = (threadIdx.x & 63) >> 4;
   bf16x8 xf[P][4];
 #pragma unroll
@@ -298,13 +304,15 @@ __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* x
         f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int d = q * DG; d < (q + 1) * DG; ++d) {
-          const bf16x8 b = int4_to_bf16(q4[d]);
+          const bf16x8 b = int4_to_bf16(q4[d], bits);
 #pragma unroll
           for (int p = 0; p < P; ++p)
             v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, v, 0, 0, 0);
         }
-        float s = bits_to_f32(one_scale ? sc[t].u16(0) : sc[t].u16(u * GM + q), scale_elem);
-        const float z = z0 + (float)(one_scale ? zc[t].u8(0) : zc[t].u8(u * GM + q));
+        // a row of one scale has a window of its own (RAG)
+        const int k = u * GM + q;
+        float s = bits_to_f32(RAG && one_scale ? sc[t].u16(0) : sc[t].u16(k), SE);
+        const float z = z0 + (float)(RAG && one_scale ? zc[t].u8(0) : zc[t].u8(k));
         if (RAG && !one_scale && q >= valid) s = 0.f;  // past the row's end
 #pragma unroll
         for (int j = 0; j < (ONE ? 1 : 4); ++j) acc[t][j] += s * (v[j] - z * xsum[q][j]);
@@ -322,7 +330,7 @@ constexpr int kNone = (int)0x80000000;  // past every buffer
 // Grid: x the first of `run` output tiles; y the route whose expert to take (R
 // <= E; only the expert's first route works), the expert (R > E; y = E: the
 // routes without an expert here), or the block of `tile` tokens (no ids).
-template <int FMT, int XE, int GM, bool RAG, int NT, bool SWIGLU, int D>
+template <int FMT, int XE, int SE, int GM, bool RAG, int NT, bool SWIGLU, int D>
 __global__ void __launch_bounds__(kThreads, GM > 1 ? 2 : NT == 2 && D == 4 && (RAG || XE != ELEM_BF16) ? 3 : 4)
 k_w4(W4Args a, int tile, int run) {
   constexpr int P = parts<XE>();
@@ -541,6 +549,7 @@ k_w4(W4Args a, int tile, int run) {
     };
 
     f32x4 acc[NT];
+    const Int4Bits bits;
 
     // the tokens' loads go first: loads return in order, so they are waited for
     // while the weights are still on their way
@@ -572,9 +581,9 @@ k_w4(W4Args a, int tile, int run) {
           for (int u = 0; u < D; ++u) {
             const int step = part + wave * S + i + u;
             if (step < KS)
-              step_product<FMT, GM, RAG, P, NT, D, false>(
+              step_product<FMT, GM, RAG, P, NT, D, false, SE>(
                   acc, xa + (wave * S + i + u) * 128, nt * xrow, nullptr, wq[u], sc, zc, u,
-                  KG - step * SG, one_scale, z0, a.scale_elem);
+                  KG - step * SG, one_scale, z0, bits);
             weights_request(u);
           }
           if (next_round(pw)) weight_rows();
@@ -636,7 +645,7 @@ constexpr int token_lds() {
   return 2 * kTokenPart * 2 + (FMT == W4_INT ? kTokenPart / 128 * GM * 4 : 0);
 }
 
-template <int FMT, int GM, bool RAG>
+template <int FMT, int SE, int GM, bool RAG>
 __global__ void __launch_bounds__(kTokenWaves * 64, 2)
 k_w4_token(W4Args a, const float* __restrict__ weights) {
   constexpr int D = 8, P = 2, SB = scale_bytes<FMT>(), SG = step_scales<FMT, GM>();
@@ -652,6 +661,7 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
   const bool has_zero = FMT == W4_INT && a.zero;
   const float z0 = has_zero ? 128.f : 136.f;
   const bool one_scale = GM == 1 && FMT == W4_INT && KG == 1;
+  const Int4Bits bits;
   float sum = 0.f;  // the product's rows all hold the token; the first is taken
 
   for (int q = wave; q < a.top_k; q += waves) {
@@ -720,9 +730,9 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
           if (s0 + u < KS)
-            step_product<FMT, GM, RAG, P, 1, D, true>(
+            step_product<FMT, GM, RAG, P, 1, D, true, SE>(
                 acc, xs + (s0 + u) * 128 - k0, xrow, sums + ((s0 + u) - k0 / 128) * GM, wq[u], sc,
-                zc, u, KG - (s0 + u) * SG, one_scale, z0, a.scale_elem);
+                zc, u, KG - (s0 + u) * SG, one_scale, z0, bits);
           weights_request(u, s0 + u + D);
         }
       }
@@ -774,7 +784,7 @@ k_w4_combine(const float* __restrict__ y, const int32_t* __restrict__ ids,
   for (int i = 0; i < 4; ++i) store_out(out, at + i, s[i], oelem);
 }
 
-template <int FMT, int XE, int GM, bool RAG, int NT, bool SWIGLU, int D>
+template <int FMT, int XE, int SE, int GM, bool RAG, int NT, bool SWIGLU, int D>
 hipError_t launch_one(const W4Args& a, int tile, hipStream_t stream) {
   const int out_n = SWIGLU ? a.N / 2 : a.N, cols = SWIGLU ? 16 : 16 * NT;
   const int tiles = (out_n + cols - 1) / cols;
@@ -783,22 +793,22 @@ hipError_t launch_one(const W4Args& a, int tile, hipStream_t stream) {
   const int64_t all = (int64_t)tiles * y;
   const int run = all < 4096 ? 1 : all < 8192 ? 2 : 4;
   const int lds = kTokenLds + (kWaves - 1) * NT * 1024 + (a.ids ? (a.R * 2 + 15) / 16 * 16 : 0);
-  hipLaunchKernelGGL((k_w4<FMT, XE, GM, RAG, NT, SWIGLU, D>), dim3((tiles + run - 1) / run, y),
+  hipLaunchKernelGGL((k_w4<FMT, XE, SE, GM, RAG, NT, SWIGLU, D>), dim3((tiles + run - 1) / run, y),
                      dim3(kThreads), lds, stream, a, tile, run);
   return hipGetLastError();
 }
 
-template <int FMT, int XE, int GM, bool RAG, bool DEEP>
+template <int FMT, int XE, int SE, int GM, bool RAG, bool DEEP>
 hipError_t launch_shape(const W4Args& a, int tile, hipStream_t stream) {
   if constexpr (XE == ELEM_PARTS) {
-    return launch_one<FMT, XE, GM, RAG, 2, false, DEEP ? 4 : 2>(a, tile, stream);
+    return launch_one<FMT, XE, SE, GM, RAG, 2, false, DEEP ? 4 : 2>(a, tile, stream);
   } else {
-    if (a.swiglu) return launch_one<FMT, XE, GM, RAG, 2, true, DEEP ? 4 : 2>(a, tile, stream);
-    return launch_one<FMT, XE, GM, RAG, 1, false, DEEP ? 4 : 2>(a, tile, stream);
+    if (a.swiglu) return launch_one<FMT, XE, SE, GM, RAG, 2, true, DEEP ? 4 : 2>(a, tile, stream);
+    return launch_one<FMT, XE, SE, GM, RAG, 1, false, DEEP ? 4 : 2>(a, tile, stream);
   }
 }
 
-template <int FMT, int XE, int GM, bool RAG>
+template <int FMT, int XE, int SE, int GM, bool RAG>
 hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   // Tokens of one pass over the weights: 16, or 8 of two parts, so that two
   // steps of them fit the LDS.  Where the experts have few routes on average,
@@ -812,24 +822,24 @@ hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   if (tokens < tile) tile = tokens;
   const int steps = ((a.K + kUnit - 1) / kUnit + 3) / 4 * 4;
   const bool whole = (kTokenLds / (parts<XE>() * tile * 2) - kPad) / kUnit >= steps;
-  if (whole) return launch_shape<FMT, XE, GM, RAG, true>(a, tile, stream);
-  return launch_shape<FMT, XE, GM, RAG, false>(a, tile, stream);
+  if (whole) return launch_shape<FMT, XE, SE, GM, RAG, true>(a, tile, stream);
+  return launch_shape<FMT, XE, SE, GM, RAG, false>(a, tile, stream);
 }
 
-template <int XE>
+template <int XE, int SE>
 hipError_t launch_format(int format, const W4Args& a, hipStream_t stream) {
   const bool ragged = a.K % 512 || a.group == a.K;
   if (format == W4_MX)
-    return ragged ? launch_walk<W4_MX, XE, 1, true>(a, stream)
-                  : launch_walk<W4_MX, XE, 1, false>(a, stream);
+    return ragged ? launch_walk<W4_MX, XE, ELEM_BF16, 1, true>(a, stream)
+                  : launch_walk<W4_MX, XE, ELEM_BF16, 1, false>(a, stream);
   if (a.group == 32)
-    return ragged ? launch_walk<W4_INT, XE, 4, true>(a, stream)
-                  : launch_walk<W4_INT, XE, 4, false>(a, stream);
+    return ragged ? launch_walk<W4_INT, XE, SE, 4, true>(a, stream)
+                  : launch_walk<W4_INT, XE, SE, 4, false>(a, stream);
   if (a.group == 64)
-    return ragged ? launch_walk<W4_INT, XE, 2, true>(a, stream)
-                  : launch_walk<W4_INT, XE, 2, false>(a, stream);
-  return ragged ? launch_walk<W4_INT, XE, 1, true>(a, stream)
-                : launch_walk<W4_INT, XE, 1, false>(a, stream);
+    return ragged ? launch_walk<W4_INT, XE, SE, 2, true>(a, stream)
+                  : launch_walk<W4_INT, XE, SE, 2, false>(a, stream);
+  return ragged ? launch_walk<W4_INT, XE, SE, 1, true>(a, stream)
+                : launch_walk<W4_INT, XE, SE, 1, false>(a, stream);
 }
 
 }  // namespace
@@ -838,16 +848,17 @@ hipError_t launch_w4(int format, const W4Args& args, hipStream_t stream) {
   if (args.R == 0) return hipSuccess;
   W4Args a = args;
   a.inv_top_k = (uint32_t)(((uint64_t(1) << 32) + a.top_k - 1) / a.top_k);
-  if (a.xelem == ELEM_PARTS) return launch_format<ELEM_PARTS>(format, a, stream);
-  if (a.xelem == ELEM_F16) return launch_format<ELEM_F16>(format, a, stream);
-  return launch_format<ELEM_BF16>(format, a, stream);
+  if (a.xelem == ELEM_F16) return launch_format<ELEM_F16, ELEM_F16>(format, a, stream);
+  if (a.xelem == ELEM_BF16) return launch_format<ELEM_BF16, ELEM_BF16>(format, a, stream);
+  if (a.scale_elem == ELEM_F16) return launch_format<ELEM_PARTS, ELEM_F16>(format, a, stream);
+  return launch_format<ELEM_PARTS, ELEM_BF16>(format, a, stream);
 }
 
 namespace {
 
-template <int FMT, int GM, bool RAG>
+template <int FMT, int SE, int GM, bool RAG>
 hipError_t launch_token(const W4Args& a, const float* weights, int T, hipStream_t stream) {
-  auto* kernel = k_w4_token<FMT, GM, RAG>;
+  auto* kernel = k_w4_token<FMT, SE, GM, RAG>;
   // eight waves take a little over the default limit of 64 KiB: raised once on
   // each device
   static std::atomic<uint64_t> raised{0};
@@ -869,10 +880,18 @@ hipError_t launch_token(const W4Args& a, const float* weights, int T, hipStream_
   return hipGetLastError();
 }
 
-template <int FMT, int GM>
+template <int FMT, int SE, int GM>
 hipError_t launch_token(const W4Args& a, const float* weights, int T, hipStream_t stream) {
-  return a.K % 512 || a.group == a.K ? launch_token<FMT, GM, true>(a, weights, T, stream)
-                                     : launch_token<FMT, GM, false>(a, weights, T, stream);
+  return a.K % 512 || a.group == a.K
+             ? launch_token<FMT, SE, GM, true>(a, weights, T, stream)
+             : launch_token<FMT, SE, GM, false>(a, weights, T, stream);
+}
+
+template <int SE>
+hipError_t launch_token_int4(const W4Args& a, const float* weights, int T, hipStream_t stream) {
+  if (a.group == 32) return launch_token<W4_INT, SE, 4>(a, weights, T, stream);
+  if (a.group == 64) return launch_token<W4_INT, SE, 2>(a, weights, T, stream);
+  return launch_token<W4_INT, SE, 1>(a, weights, T, stream);
 }
 
 }  // namespace
@@ -883,10 +902,9 @@ hipError_t launch_w4_down(int format, const W4Args& a, const float* weights, flo
   // either way (mx, 256 experts, top-6: 40.0 us against 44.0 for two tokens, 75
   // against 75 for four; 8 experts, top-2, four tokens: 23.8 against 28.2).
   if (T <= kW4TokenMax) {
-    if (format == W4_MX) return launch_token<W4_MX, 1>(a, weights, T, stream);
-    if (a.group == 32) return launch_token<W4_INT, 4>(a, weights, T, stream);
-    if (a.group == 64) return launch_token<W4_INT, 2>(a, weights, T, stream);
-    return launch_token<W4_INT, 1>(a, weights, T, stream);
+    if (format == W4_MX) return launch_token<W4_MX, ELEM_BF16, 1>(a, weights, T, stream);
+    return a.scale_elem == ELEM_F16 ? launch_token_int4<ELEM_F16>(a, weights, T, stream)
+                                    : launch_token_int4<ELEM_BF16>(a, weights, T, stream);
   }
   W4Args down = a;
   down.out = y;
