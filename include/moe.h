@@ -552,7 +552,8 @@ int fused_moe_down_combine(int32_t dtype, const void* w2, const void* w2_scale,
  *                    then n_shared shared ones, ids T*top_k + t*n_shared + s
  *                    (moe_align_shared; 0 for moe_align's plans).
  *   rows_cap         rows of the row buffers and of sorted_token_ids
- *                    (moe_align_capacity's *sorted_cap).
+ *                    (moe_align_capacity's *sorted_cap; a smaller one must not
+ *                    be below *num_tokens_post_padded).
  *   sorted_token_ids, num_tokens_post_padded
  *                    the planner's outputs, read on the device.
  *   row_of_route     (T * (top_k + n_shared)) int32: moe_route_rows' output
@@ -623,7 +624,7 @@ int moe_unpermute_backward(int32_t elem, const void* d_out, const void* rows,
  *                    w_j (d_weights_j - sum_i w_i d_weights_i),
  * zeros elsewhere; (T, E) fp32, every element written.  The selection itself
  * has no gradient.  An id outside [0, E) takes part in the inner sum only.
- * E <= 1024, top_k <= 16, T < 2^26.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE,
+ * E <= 1024, top_k <= 16, T <= 2^26 - 4.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE,
  * MOE_ERR_UNSUPPORTED, MOE_ERR_ALIGN, MOE_ERR_HIP. */
 int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const float* d_weights,
                        float* d_logits, int64_t T, int32_t E, int32_t top_k, void* stream);

@@ -590,6 +590,8 @@ def moe_route_rows(topk_ids, num_experts, sorted_token_ids, num_tokens_post_padd
     T, k = _matrix(topk_ids, "topk_ids")
     dev = topk_ids.device
     _on_gpu(topk_ids, "topk_ids")
+    if n_shared < 0:
+        raise MoeError(-2, f"n_shared must be >= 0 (got {n_shared})")
     cap = sorted_token_ids.numel()
     ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
     plan = _operand(sorted_token_ids, "sorted_token_ids", torch.int32, (cap,), dev)
@@ -694,6 +696,8 @@ def moe_route_backward(topk_ids, topk_weights, d_weights, num_experts, stream=No
     ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
     w = _operand(topk_weights, "topk_weights", torch.float32, (T, k), dev)
     d = _operand(d_weights, "d_weights", torch.float32, (T, k), dev)
+    if num_experts < 1:
+        raise MoeError(-2, f"num_experts must be >= 1 (got {num_experts})")
     out = _output(out, "out", (T, num_experts), torch.float32, dev, stream)
     _enqueue(lib().moe_route_backward, dev, stream, ids, w, d, out.data_ptr(), T, num_experts, k)
     return out
@@ -739,6 +743,8 @@ def moe_w4_matvec(fmt, x, w, w_scale, w_zero, topk_ids, group, swiglu=False, str
     if w.dim() != 3:
         raise MoeError(-2, f"w must have shape (E, N, K/2) (got {tuple(w.shape)})")
     E, N, _ = w.shape
+    if x.dim() not in (2, 3):
+        raise MoeError(-2, f"x must have shape (T, K) or (T, top_k, K) (got {tuple(x.shape)})")
     T, K = x.shape[0], x.shape[-1]
     n = N // 2 if swiglu else N
     if topk_ids is None:

@@ -139,8 +139,8 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const
   if (T < 0) return abi_fail(MOE_ERR_SHAPE, "T must be >= 0 (got %lld)", (long long)T);
   if (E < 1) return abi_fail(MOE_ERR_SHAPE, "E must be >= 1 (got %d)", E);
   if (top_k < 1) return abi_fail(MOE_ERR_SHAPE, "top_k must be >= 1 (got %d)", top_k);
-  if (T >= (int64_t(1) << 26))
-    return abi_fail(MOE_ERR_UNSUPPORTED, "moe_route_backward needs T < 2^26");
+  if ((T + 3) / 4 > kMaxGroups)  // a workgroup has four tokens
+    return abi_fail(MOE_ERR_UNSUPPORTED, "moe_route_backward needs T <= 2^26 - 4");
   if (E > 1024) return abi_fail(MOE_ERR_UNSUPPORTED, "moe_route_backward supports E <= 1024 (got %d)", E);
   if (top_k > 16)
     return abi_fail(MOE_ERR_UNSUPPORTED, "moe_route_backward needs top_k <= 16 (got %d)", top_k);

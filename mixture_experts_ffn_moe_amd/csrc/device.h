@@ -244,6 +244,13 @@ __device__ __forceinline__ float max_dpp(float v) {
   return __builtin_fmaxf(v, __int_as_float(u));
 }
 
+// Orders a wave's LDS accesses of different lanes: the hardware keeps a wave's
+// LDS operations in order, this keeps the compiler from moving them.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // v plus the value lane movement CTRL (a DPP control) brings in
 template <int CTRL>
 __device__ __forceinline__ float add_dpp(float v) {

@@ -371,9 +371,9 @@ k_route_backward(const int32_t* __restrict__ ids, const float* __restrict__ w,
     const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
     if (id == ij) s += dj;
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_fence();
   if (lane < top_k && (unsigned)id < (unsigned)E) line[id] = s;
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_fence();
   float* row = d_logits + t * E;
   constexpr int V = A / 4;
   for (int e = lane * V; e < E; e += 64 * V) {
@@ -415,7 +415,7 @@ template <int ELEM, int A, bool STREAM>
 void unpermute_backward(const RowsArgs& a, const void* d_out, const void* rows, void* d_rows,
                         float* d_w, hipStream_t stream) {
   constexpr int JB = 8;
-  const int JG = (a.top_k + a.n_shared + JB - 1) / JB;
+  const int JG = (int)(((int64_t)a.top_k + a.n_shared + JB - 1) / JB);
   const dim3 grid((unsigned)(a.T * JG + (a.cap + kPadRows - 1) / kPadRows));
   auto g = static_cast<const uint8_t*>(d_out);
   auto y = static_cast<const uint8_t*>(rows);

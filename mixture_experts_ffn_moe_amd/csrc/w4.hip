@@ -728,7 +728,7 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
           if (lane % (16 / GM) == 0) sums[(i * 512 + lane * 8) / (128 / GM)] = v;
         }
       }
-      __builtin_amdgcn_wave_barrier();  // the wave's own LDS, in order
+      wave_lds_fence();  // the wave's own LDS
       const int end = min(KS, (k0 + kTokenPart) / 128);
       for (int s0 = k0 / 128; s0 < end; s0 += D) {
         sc[0] = sn[0];
@@ -747,7 +747,7 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
           weights_request(u, s0 + u + D);
         }
       }
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_fence();
     }
     sum += weights[r] * acc[0][0];
   }

@@ -145,3 +145,19 @@ def test_binding_refuses():
         with pytest.raises(moe.MoeError) as e:
             call()
         assert e.value.status == status, (n, str(e.value))
+
+
+def test_one_launch_holds_the_call():
+    # four tokens a workgroup, and a launch has less than 2^24 of them
+    assert route_backward(T=(1 << 26) - 3) == UNSUPPORTED
+    assert b"2^26" in moe.lib().moe_last_error()
+
+
+def test_binding_refuses_negative_counts():
+    i32, f32 = torch.int32, torch.float32
+    plan, ntp, ids, w = Fake((64,), i32), Fake((1,), i32), Fake((4, 2), i32), Fake((4, 2), f32)
+    for call in (lambda: moe.moe_route_rows(ids, 8, plan, ntp, n_shared=-3),
+                 lambda: moe.moe_route_backward(ids, w, w, -1)):
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.status == SHAPE

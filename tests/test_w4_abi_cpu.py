@@ -102,3 +102,15 @@ def test_binding_refuses():
         with pytest.raises(moe.MoeError) as e:
             call()
         assert e.value.status == status, (n, str(e.value))
+
+
+def test_binding_refuses_other_ranks():
+    u8, i32 = torch.uint8, torch.int32
+    w, s, ids = Fake((4, 64, 128), u8), Fake((4, 64, 2)), Fake((2, 2), i32)
+    w.dim = lambda: 3
+    for shape in ((), (256,), (1, 2, 2, 256)):
+        x = Fake(shape)
+        x.dim = lambda: len(shape)
+        with pytest.raises(moe.MoeError) as e:
+            moe.moe_w4_matvec("int4", x, w, s, None, ids, 128)
+        assert e.value.status == SHAPE
