@@ -831,9 +831,20 @@ hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   if (a.ids && a.R <= a.E) tile = 4;
   else if (a.ids && a.R <= 2 * (int64_t)a.E) tile /= 2;
   if (tokens < tile) tile = tokens;
-  const int steps = ((a.K + kUnit - 1) / kUnit + 3) / 4 * 4;
-  const bool whole = (kTokenLds / (parts<XE>() * tile * 2) - kPad) / kUnit >= steps;
-  if (whole) return launch_shape<FMT, XE, SE, GM, RAG, true>(a, tile, stream);
+  // Four steps ahead, where the tokens' K fits the LDS whole, or two.  A round of
+  // four that a wave has one or two steps of loads the last one again for the
+  // others: two is better there (40 routes of 64 experts, groups of 128, first
+  // product: K = 1024 17.5 us against 20.2, 2048 38.1 against 35.4).  Narrow groups
+  // are short of vector instructions before they are short of loads in flight
+  // (groups of 32, 2048: 43.4 against 49.0; 4096: 83.3 against 81.2), and so is
+  // the second product, which holds the tokens in two parts (groups of 64, 2048:
+  // 28.6 against 33.3; e2m1 22.7 against 24.2; groups of 128 26.8 against 26.4).
+  const int steps = (a.K + kUnit - 1) / kUnit, last = steps % 4;
+  const int held = (kTokenLds / (parts<XE>() * tile * 2) - kPad) / kUnit;
+  if constexpr (XE != ELEM_PARTS || (FMT == W4_INT && GM == 1)) {
+    if (held >= (steps + 3) / 4 * 4 && (last == 0 || last == 3) && (GM < 4 || steps > 6))
+      return launch_shape<FMT, XE, SE, GM, RAG, true>(a, tile, stream);
+  }
   return launch_shape<FMT, XE, SE, GM, RAG, false>(a, tile, stream);
 }
 
