@@ -61,8 +61,11 @@ constexpr int kUnit = kWaves * 128;     // K elements of one step of every wave
 constexpr int kPad = 8;                 // elements behind each token's row in LDS
 constexpr int kBlocks = 4;              // 64-route blocks found without a barrier
 // LDS of the tokens: a few tokens' whole K, or 1,024 elements of kTile tokens
-// (half as many of two parts).
+// (half as many of two parts); and the most that the sums and the list leave.
 constexpr int kTokenLds = kTile * (2 * kUnit + kPad) * 2;
+constexpr int kTokenLdsMost = 144 * 1024;
+constexpr int kSumLds = (kWaves - 1) * 2 * 1024;  // the waves' sums of two tiles
+constexpr int kCUs = 256, kLds = 160 * 1024;      // of a CU
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -343,13 +346,13 @@ constexpr int kNone = (int)0x80000000;  // past every buffer
 template <int FMT, int XE, int SE, int GM, bool RAG, int NT, bool SWIGLU, int D>
 __global__ void
 __launch_bounds__(kThreads, GM > 1 ? 2 : NT == 2 && D == 4 && (RAG || XE != ELEM_BF16) ? 3 : 4)
-k_w4(W4Args a, int tile, int run) {
+k_w4(W4Args a, int tile, int run, int token_lds) {
   constexpr int P = parts<XE>();
   constexpr int kRowParts = XE == ELEM_PARTS ? 2 : 1;  // 16-bit rows of a token in memory
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* xs = reinterpret_cast<uint16_t*>(smem);
-  float* red = reinterpret_cast<float*>(smem + kTokenLds);  // waves 1.. of each tile
-  uint16_t* list = reinterpret_cast<uint16_t*>(smem + kTokenLds + (kWaves - 1) * NT * 1024);
+  float* red = reinterpret_cast<float*>(smem + token_lds);  // waves 1.. of each tile
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + token_lds + (kWaves - 1) * NT * 1024);
   __shared__ int wave_count[kWaves];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
@@ -440,7 +443,7 @@ k_w4(W4Args a, int tile, int run) {
   for (int m0 = 0; m0 < count; m0 += tile) {
     const int nt = min(tile, count - m0);
     // steps of each wave in one part of K: what the LDS holds for nt tokens
-    const int fit = (kTokenLds / (P * nt * 2) - kPad) / kUnit;
+    const int fit = (token_lds / (P * nt * 2) - kPad) / kUnit;
     const bool whole = D > 2 || fit >= JP;  // many steps ahead only where K fits
     const int S = whole ? JP : fit / D * D;  // fit >= D: the launch sees to it
     const int xrow = S * kUnit + kPad, inv_s = 65536 / S + 1;  // seg * inv_s >> 16 = seg / S
@@ -795,27 +798,58 @@ k_w4_combine(const float* __restrict__ y, const int32_t* __restrict__ ids,
   for (int i = 0; i < 4; ++i) store_out(out, at + i, s[i], oelem);
 }
 
+// Lets Kernel have `bytes` of dynamic LDS past the default limit of 64 KiB: once
+// on each device.
+template <auto* Kernel>
+hipError_t allow_lds(int bytes) {
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev <= 63 && (raised.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kernel),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) raised.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// Output tiles, the grid's y and the bytes of a workgroup's list of routes.
+template <int XE>
+int out_tiles(const W4Args& a) {
+  const int cols = XE == ELEM_PARTS ? 32 : 16;
+  return ((a.swiglu ? a.N / 2 : a.N) + cols - 1) / cols;
+}
+int list_bytes(const W4Args& a) { return a.ids ? (a.R * 2 + 15) / 16 * 16 : 0; }
+int grid_y(const W4Args& a, int tile) {
+  return !a.ids ? (a.R + tile - 1) / tile : a.R <= a.E ? a.R : a.E + 1;
+}
+
 template <int FMT, int XE, int SE, int GM, bool RAG, int NT, bool SWIGLU, int D>
-hipError_t launch_one(const W4Args& a, int tile, hipStream_t stream) {
-  const int out_n = SWIGLU ? a.N / 2 : a.N, cols = SWIGLU ? 16 : 16 * NT;
-  const int tiles = (out_n + cols - 1) / cols;
-  const int y = !a.ids ? (a.R + tile - 1) / tile : a.R <= a.E ? a.R : a.E + 1;
+hipError_t launch_one(const W4Args& a, int tile, int token_lds, hipStream_t stream) {
+  const int tiles = out_tiles<XE>(a), y = grid_y(a, tile);
   // several tiles a workgroup once there are more workgroups than the GPU holds
   const int64_t all = (int64_t)tiles * y;
   const int run = all < 4096 ? 1 : all < 8192 ? 2 : 4;
-  const int lds = kTokenLds + (kWaves - 1) * NT * 1024 + (a.ids ? (a.R * 2 + 15) / 16 * 16 : 0);
-  hipLaunchKernelGGL((k_w4<FMT, XE, SE, GM, RAG, NT, SWIGLU, D>), dim3((tiles + run - 1) / run, y),
-                     dim3(kThreads), lds, stream, a, tile, run);
+  const int lds = token_lds + (kWaves - 1) * NT * 1024 + list_bytes(a);
+  constexpr auto kernel = k_w4<FMT, XE, SE, GM, RAG, NT, SWIGLU, D>;
+  if (lds > 65536) {
+    const hipError_t e = allow_lds<kernel>(kTokenLdsMost + kSumLds + kW4MaxRoutes * 2);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3((tiles + run - 1) / run, y), dim3(kThreads), lds, stream, a, tile,
+                     run, token_lds);
   return hipGetLastError();
 }
 
 template <int FMT, int XE, int SE, int GM, bool RAG, bool DEEP>
-hipError_t launch_shape(const W4Args& a, int tile, hipStream_t stream) {
+hipError_t launch_shape(const W4Args& a, int tile, int token_lds, hipStream_t stream) {
+  constexpr int D = DEEP ? 4 : 2;
   if constexpr (XE == ELEM_PARTS) {
-    return launch_one<FMT, XE, SE, GM, RAG, 2, false, DEEP ? 4 : 2>(a, tile, stream);
+    return launch_one<FMT, XE, SE, GM, RAG, 2, false, D>(a, tile, token_lds, stream);
   } else {
-    if (a.swiglu) return launch_one<FMT, XE, SE, GM, RAG, 2, true, DEEP ? 4 : 2>(a, tile, stream);
-    return launch_one<FMT, XE, SE, GM, RAG, 1, false, DEEP ? 4 : 2>(a, tile, stream);
+    if (a.swiglu) return launch_one<FMT, XE, SE, GM, RAG, 2, true, D>(a, tile, token_lds, stream);
+    return launch_one<FMT, XE, SE, GM, RAG, 1, false, D>(a, tile, token_lds, stream);
   }
 }
 
@@ -840,12 +874,23 @@ hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   // the second product, which holds the tokens in two parts (groups of 64, 2048:
   // 28.6 against 33.3; e2m1 22.7 against 24.2; groups of 128 26.8 against 26.4).
   const int steps = (a.K + kUnit - 1) / kUnit, last = steps % 4;
-  const int held = (kTokenLds / (parts<XE>() * tile * 2) - kPad) / kUnit;
+  const int rounded = (steps + 3) / 4 * 4, row = parts<XE>() * tile * 2;
+  // More LDS for the tokens, so that K fits whole, where all workgroups still
+  // find a place at once (8 tokens of 4096 x 4096 in groups of 128: 7.7 us against
+  // 8.5, 16 tokens 10.3 against 11.3; 16 fp16 ones, which no longer do, 28.0
+  // against 19.3).
+  const int64_t whole = row * ((int64_t)rounded * kUnit + kPad);
+  const int64_t groups = (int64_t)out_tiles<XE>(a) * grid_y(a, tile);
+  int token_lds = kTokenLds;
+  if (whole > kTokenLds && whole <= kTokenLdsMost &&
+      groups <= kCUs * (kLds / (whole + kSumLds + list_bytes(a) + 64)))
+    token_lds = (int)(whole + 15) / 16 * 16;
+  const int held = (token_lds / row - kPad) / kUnit;
   if constexpr (XE != ELEM_PARTS || (FMT == W4_INT && GM == 1)) {
-    if (held >= (steps + 3) / 4 * 4 && (last == 0 || last == 3) && (GM < 4 || steps > 6))
-      return launch_shape<FMT, XE, SE, GM, RAG, true>(a, tile, stream);
+    if (held >= rounded && (last == 0 || last == 3) && (GM < 4 || steps > 6))
+      return launch_shape<FMT, XE, SE, GM, RAG, true>(a, tile, token_lds, stream);
   }
-  return launch_shape<FMT, XE, SE, GM, RAG, false>(a, tile, stream);
+  return launch_shape<FMT, XE, SE, GM, RAG, false>(a, tile, token_lds, stream);
 }
 
 template <int XE, int SE>
@@ -880,21 +925,10 @@ namespace {
 
 template <int FMT, int SE, int GM, bool RAG>
 hipError_t launch_token(const W4Args& a, const float* weights, int T, hipStream_t stream) {
-  auto* kernel = k_w4_token<FMT, SE, GM, RAG>;
-  // eight waves take a little over the default limit of 64 KiB: raised once on
-  // each device
-  static std::atomic<uint64_t> raised{0};
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
+  constexpr auto kernel = k_w4_token<FMT, SE, GM, RAG>;
+  // eight waves take a little over the default limit
+  const hipError_t e = allow_lds<kernel>(kTokenWaves * token_lds<FMT, GM>());
   if (e != hipSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (dev > 63 || !(raised.load(std::memory_order_relaxed) & bit)) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                            kTokenWaves * token_lds<FMT, GM>());
-    if (e != hipSuccess) return e;
-    raised.fetch_or(bit, std::memory_order_relaxed);
-  }
   const int waves = a.top_k < kTokenWaves ? a.top_k : kTokenWaves;
   constexpr int lds = token_lds<FMT, GM>();
   hipLaunchKernelGGL(kernel, dim3((a.N + 15) / 16, T), dim3(waves * 64), waves * lds, stream, a,

@@ -127,3 +127,25 @@ def test_expert_past_4_gib():
     got = moe.moe_w4_matvec("int4", X, w, s, z, ids, 128).double().cpu().numpy()
     d = w4.dequant("int4", *[v[0] for v in W], 128)
     assert np.array_equal(got[:, 0], rounded(x @ d.T, "bf16"))
+
+
+@pytest.mark.parametrize("fmt,group", [("int4", 128), ("int4", 32), ("mx", 32)])
+@pytest.mark.parametrize("elem,T,k,E,K,N", [
+    ("bf16", 16, 1, 1, 4096, 72), ("bf16", 11, 1, 1, 4480, 64), ("f16", 8, 1, 1, 4096, 40),
+    ("f16", 13, 1, 1, 1152, 4100), ("bf16", 16, 2, 8, 4096, 64), ("bf16", 150, 2, 8, 2048, 50),
+    ("bf16", 2048, 2, 4, 4096, 32)])
+def test_tokens_held_whole(fmt, group, elem, T, k, E, K, N):
+    """Few output tiles of many tokens: the whole of K in a larger LDS; exact."""
+    rng = np.random.default_rng(K + T)
+    W, D = weights(fmt, group, fmt == "int4", E, N, K, elem, rng, exact=True)
+    x, X = activations((T, K), elem, rng, exact=True)
+    x, X = np.clip(x, -2, 2), X.clamp(-2, 2)
+    ids = rng.integers(-1, E, (T, k)).astype(np.int32) if E > 1 else None
+    got = moe.moe_w4_matvec(fmt, X, *D, None if ids is None else torch.from_numpy(ids).cuda(), group)
+    got = got.double().cpu().numpy().reshape(T, k, N)
+    for e in range(E):
+        t, j = np.nonzero(ids == e) if E > 1 else (np.arange(T), np.zeros(T, int))
+        d = w4.dequant(fmt, *[None if v is None else v[e] for v in W], group)
+        assert np.array_equal(got[t, j], rounded(x[t] @ d.T, elem)), e
+    if E > 1:
+        assert not got[ids < 0].any()
