@@ -149,3 +149,31 @@ def test_tokens_held_whole(fmt, group, elem, T, k, E, K, N):
         assert np.array_equal(got[t, j], rounded(x[t] @ d.T, elem)), e
     if E > 1:
         assert not got[ids < 0].any()
+
+
+def test_first_call_captured():
+    """A call whose kernels ask for more LDS than the default, in a graph with
+    no eager call before it."""
+    rng = np.random.default_rng(8)
+    K, I, E, k = 256, 128, 9, 8
+    _, D1 = weights("int4", 0, True, E, 2 * I, K, "f16", rng)
+    _, D2 = weights("int4", 0, True, E, K, I, "f16", rng)
+    _, DL = weights("int4", 0, True, 1, 64, 4096, "f16", rng)
+    x = torch.randn(1, K, device="cuda").half()
+    xl = torch.randn(8, 4096, device="cuda").half()
+    ids = torch.arange(8, dtype=torch.int32, device="cuda").reshape(1, k)
+    w = torch.full((1, k), 0.125, device="cuda")
+    out, lin = torch.empty_like(x), torch.empty(8, 64, dtype=torch.float16, device="cuda")
+    ws = torch.empty(moe.moe_w4_workspace_size(1, K, 2 * I, k), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.fused_moe_w4("int4", x, *D1, *D2, ids, w, 0, out=out, workspace=ws)
+        moe.moe_w4_matvec("int4", xl, *DL, None, 0, out=lin)
+    for seed in (1, 2, 3):
+        x.copy_(torch.randn(1, K, generator=torch.Generator().manual_seed(seed)))
+        xl.copy_(torch.randn(8, 4096, generator=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, moe.fused_moe_w4("int4", x, *D1, *D2, ids, w, 0)), seed
+        assert torch.equal(lin, moe.moe_w4_matvec("int4", xl, *DL, None, 0)), seed
