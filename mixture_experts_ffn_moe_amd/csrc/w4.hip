@@ -16,12 +16,18 @@
 //         brought into LDS, cost 8 tokens of 4096 x 4096 10.2 us against 9.0).
 //         The offset costs about five of fp32's 24 bits, against the 8 or 11 of
 //         the output.
+//         With fp16 activations the codes are fp16: 1024 + q in the same way,
+//         then 1032 taken off again, exactly, by a packed subtraction.  1024 + q
+//         itself, or q 2^-24 as a subnormal, would cost the matrix instruction's
+//         sum eight bits more (measured: 2.3e-5 of the result against 3e-6).
+//         Two bf16 parts of the activations, the alternative, are twice the matrix
+//         instructions and LDS: 32 tokens of 4096 x 8192 51 us against 20.6.
 //   e2m1: the hardware's conversion, scale included; e2m1 times a power of
 //         two is a bf16, so this is exact too.
-// Activations are bf16 operands: bf16 ones as they are, fp16 ones as two bf16
-// parts hi + lo, which is exact.  The FFN's intermediate, an fp32 value, is
-// written as two such parts (2^-17 of it is lost), in the order the second
-// product reads.
+// Activations are operands as they are, except fp16 ones with e2m1 (whose scales
+// are out of fp16's range): two bf16 parts hi + lo, which is exact.  The FFN's
+// intermediate, an fp32 value, is written as two such parts (2^-17 of it is
+// lost), in the order the second product reads.
 //
 // A 16x16x32 matrix instruction takes 16 tokens (A rows) and 16 weight rows (B
 // columns); a lane (n = l % 16, g = l / 16) reads 16 bytes of row n in each
@@ -48,6 +54,7 @@
 // weights past the caches was slower (366 -> 381 us for the e2m1 FFN): a line of
 // 128 bytes is read in two steps.
 #include <atomic>
+#include <type_traits>
 
 #include "device.h"
 #include "ops.h"
@@ -69,8 +76,11 @@ constexpr int kCUs = 256, kLds = 160 * 1024;      // of a CU
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-template <int XE>
-constexpr int parts() { return XE == ELEM_BF16 ? 1 : 2; }
+// fp16 activations stay fp16 where the codes can be fp16 too.
+template <int FMT, int XE>
+constexpr bool half_ops() { return FMT == W4_INT && XE == ELEM_F16; }
+template <int FMT, int XE>
+constexpr int parts() { return XE == ELEM_BF16 || half_ops<FMT, XE>() ? 1 : 2; }
 
 __device__ __forceinline__ float bits_to_f32(uint32_t u16, int elem) {
   return elem == ELEM_F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)u16)
@@ -83,16 +93,31 @@ __device__ __forceinline__ int buf_loadu16(__amdgpu_buffer_rsrc_t r, uint32_t vo
 
 // The two constants of the int4 conversion, in registers: as literals the
 // compiler takes an and and an or for each pair where one v_and_or does.
+template <bool HALF>
 struct Int4Bits {
-  uint32_t mask = 0x000F000Fu, bias = 0x43004300u;
+  uint32_t mask = 0x000F000Fu, bias = HALF ? 0x64006400u : 0x43004300u;
   __device__ __forceinline__ Int4Bits() { asm("" : "+s"(mask), "+v"(bias)); }
 };
 
-// 8 int4 codes of one dword as bf16 128 + q, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8 int4_to_bf16(uint32_t v, const Int4Bits& c) {
-  return __builtin_bit_cast(
-      bf16x8, make_uint4((v & c.mask) | c.bias, ((v >> 4) & c.mask) | c.bias,
-                         ((v >> 8) & c.mask) | c.bias, ((v >> 12) & c.mask) | c.bias));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+template <bool HALF>
+using Operand = typename std::conditional<HALF, f16x8, bf16x8>::type;
+
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// 8 int4 codes of one dword as bf16 128 + q or fp16 q - 8, in the order 0 4 1 5
+// 2 6 3 7.
+template <bool HALF>
+__device__ __forceinline__ Operand<HALF> int4_operand(uint32_t v, const Int4Bits<HALF>& c) {
+  const uint4 b = make_uint4((v & c.mask) | c.bias, ((v >> 4) & c.mask) | c.bias,
+                             ((v >> 8) & c.mask) | c.bias, ((v >> 12) & c.mask) | c.bias);
+  if constexpr (HALF) return __builtin_bit_cast(f16x8, b) - (_Float16)1032.f;
+  else return __builtin_bit_cast(bf16x8, b);
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -159,7 +184,7 @@ __device__ __forceinline__ float pair_sum(uint32_t d) {
 }
 
 // 8 activations into LDS as bf16 in that order, part 1 `part` elements after
-// part 0.  Returns their sum (int4; in fp32 as every sum here).
+// part 0.  Returns their sum (int4 with bf16 operands; in fp32 as every sum here).
 template <int FMT, int XE>
 __device__ __forceinline__ float store_tokens(const X8<XE>& x, uint16_t* to, int part) {
   const uint32_t d[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w};
@@ -167,7 +192,7 @@ __device__ __forceinline__ float store_tokens(const X8<XE>& x, uint16_t* to, int
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     b[0][i] = d[i], b[1][i] = 0;
-    if constexpr (XE == ELEM_F16) {
+    if constexpr (XE == ELEM_F16 && !half_ops<FMT, XE>()) {
       const float f = bits_to_f32(d[i] & 0xFFFFu, ELEM_F16), h = bits_to_f32(d[i] >> 16, ELEM_F16);
       const uint32_t f0 = f32_to_bf16(f), h0 = f32_to_bf16(h);
       b[0][i] = f0 | h0 << 16;
@@ -179,13 +204,13 @@ __device__ __forceinline__ float store_tokens(const X8<XE>& x, uint16_t* to, int
     b[1][0] = x.v[1].x, b[1][1] = x.v[1].y, b[1][2] = x.v[1].z, b[1][3] = x.v[1].w;
   float sum = 0.f;
 #pragma unroll
-  for (int p = 0; p < parts<XE>(); ++p) {
+  for (int p = 0; p < parts<FMT, XE>(); ++p) {
     uint4 v = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
     if constexpr (FMT != W4_MX && XE != ELEM_PARTS)
       v = make_uint4(lo_halves(b[p][0], b[p][2]), hi_halves(b[p][0], b[p][2]),
                      lo_halves(b[p][1], b[p][3]), hi_halves(b[p][1], b[p][3]));
     *reinterpret_cast<uint4*>(to + p * part) = v;
-    if constexpr (FMT != W4_MX)
+    if constexpr (FMT != W4_MX && !half_ops<FMT, XE>())
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum += pair_sum(b[p][i]);
   }
@@ -255,21 +280,21 @@ using ScaleWindow = Window<D * step_scales<FMT, GM>() * scale_bytes<FMT>(), RAG>
 // valid: the scale groups of the step that the row has (RAG).  ONE: every row
 // of the product is the same token, whose sum over group q of the step is sx[q];
 // only the first row is made.  SE: type of int4 scales.
-template <int FMT, int GM, bool RAG, int P, int NT, int D, bool ONE, int SE>
+template <int FMT, int GM, bool RAG, int P, int NT, int D, bool ONE, int SE, bool HALF>
 __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* xp, int part,
                                              const float* sx,
                                              const uint4 (&wq)[NT],
                                              const ScaleWindow<FMT, D, GM, RAG> (&sc)[NT],
                                              const ZeroWindow<D, GM, RAG> (&zc)[NT], int u,
                                              int valid, bool one_scale, float z0,
-                                             const Int4Bits& bits) {
+                                             const Int4Bits<HALF>& bits) {
   const int g = (threadIdx.x & 63) >> 4;
-  bf16x8 xf[P][4];
+  Operand<HALF> xf[P][4];
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int d = 0; d < 4; ++d)
-      xf[p][d] = *reinterpret_cast<const bf16x8*>(
+      xf[p][d] = *reinterpret_cast<const Operand<HALF>*>(
           xp + p * part + (GM == 1 ? 32 * g + 8 * d : 32 * d + 8 * g));
   if constexpr (FMT == W4_MX) {
 #pragma unroll
@@ -285,7 +310,7 @@ __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* x
         const bf16x8 b = e2m1_to_bf16(q[d], s);
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, acc[t], 0, 0, 0);
+          acc[t] = mma(xf[p][d], b, acc[t]);
       }
     }
   } else {
@@ -297,13 +322,13 @@ __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* x
       if constexpr (ONE) {
         xsum[q][0] = sx[q];
       } else {
-        const bf16x8 ones = __builtin_bit_cast(
-            bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u));
+        constexpr uint32_t one = HALF ? 0x3C003C00u : 0x3F803F80u;
+        const auto ones = __builtin_bit_cast(Operand<HALF>, make_uint4(one, one, one, one));
 #pragma unroll
         for (int d = q * DG; d < (q + 1) * DG; ++d)
 #pragma unroll
           for (int p = 0; p < P; ++p)
-            xsum[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], ones, xsum[q], 0, 0, 0);
+            xsum[q] = mma(xf[p][d], ones, xsum[q]);
       }
     }
 #pragma unroll
@@ -316,10 +341,10 @@ __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* x
         f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int d = q * DG; d < (q + 1) * DG; ++d) {
-          const bf16x8 b = int4_to_bf16(q4[d], bits);
+          const Operand<HALF> b = int4_operand<HALF>(q4[d], bits);
 #pragma unroll
           for (int p = 0; p < P; ++p)
-            v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p][d], b, v, 0, 0, 0);
+            v = mma(xf[p][d], b, v);
         }
         // a row of one scale has a window of its own (RAG)
         const int k = u * GM + q;
@@ -345,9 +370,10 @@ constexpr int kNone = (int)0x80000000;  // past every buffer
 // routes without an expert here), or the block of `tile` tokens (no ids).
 template <int FMT, int XE, int SE, int GM, bool RAG, int NT, bool SWIGLU, int D>
 __global__ void
-__launch_bounds__(kThreads, GM > 1 ? 2 : NT == 2 && D == 4 && (RAG || XE != ELEM_BF16) ? 3 : 4)
+__launch_bounds__(kThreads, GM > 1 ? 2 : NT == 2 && D == 4 && (RAG || parts<FMT, XE>() == 2) ? 3 : 4)
 k_w4(W4Args a, int tile, int run, int token_lds) {
-  constexpr int P = parts<XE>();
+  constexpr int P = parts<FMT, XE>();
+  constexpr bool HALF = half_ops<FMT, XE>();
   constexpr int kRowParts = XE == ELEM_PARTS ? 2 : 1;  // 16-bit rows of a token in memory
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* xs = reinterpret_cast<uint16_t*>(smem);
@@ -437,7 +463,7 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
   const bool has_zero = FMT == W4_INT && a.zero;
   const __amdgpu_buffer_rsrc_t rz = dword_rsrc(has_zero ? a.zero + (size_t)e * a.N * KG : a.w,
                                                has_zero ? (uint32_t)a.N * KG : 0, skip_z);
-  const float z0 = has_zero ? 128.f : 136.f;  // an empty buffer's loads read 0
+  const float z0 = (HALF ? -8.f : 128.f) + (has_zero ? 0.f : 8.f);  // an empty buffer's loads read 0
   const bool one_scale = GM == 1 && FMT == W4_INT && KG == 1;  // of the whole row
 
   for (int m0 = 0; m0 < count; m0 += tile) {
@@ -563,7 +589,7 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
     };
 
     f32x4 acc[NT];
-    const Int4Bits bits;
+    const Int4Bits<HALF> bits;
 
     // the tokens' loads go first: loads return in order, so they are waited for
     // while the weights are still on their way
@@ -595,7 +621,7 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
           for (int u = 0; u < D; ++u) {
             const int step = part + wave * S + i + u;
             if (step < KS)
-              step_product<FMT, GM, RAG, P, NT, D, false, SE>(
+              step_product<FMT, GM, RAG, P, NT, D, false, SE, HALF>(
                   acc, xa + (wave * S + i + u) * 128, nt * xrow, nullptr, wq[u], sc, zc, u,
                   KG - step * SG, one_scale, z0, bits);
             weights_request(u);
@@ -675,7 +701,7 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
   const bool has_zero = FMT == W4_INT && a.zero;
   const float z0 = has_zero ? 128.f : 136.f;
   const bool one_scale = GM == 1 && FMT == W4_INT && KG == 1;
-  const Int4Bits bits;
+  const Int4Bits<false> bits;
   float sum = 0.f;  // the product's rows all hold the token; the first is taken
 
   for (int q = wave; q < a.top_k; q += waves) {
@@ -744,7 +770,7 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
           if (s0 + u < KS)
-            step_product<FMT, GM, RAG, P, 1, D, true, SE>(
+            step_product<FMT, GM, RAG, P, 1, D, true, SE, false>(
                 acc, xs + (s0 + u) * 128 - k0, xrow, sums + ((s0 + u) - k0 / 128) * GM, wq[u], sc,
                 zc, u, KG - (s0 + u) * SG, one_scale, z0, bits);
           weights_request(u, s0 + u + D);
@@ -861,7 +887,7 @@ hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   // more routes takes another pass (T = 32, 256 experts, top-6: 369 us with
   // passes of 4, 392 with 8).
   const int tokens = a.R / a.top_k;
-  int tile = kTile / parts<XE>();
+  int tile = kTile / parts<FMT, XE>();
   if (a.ids && a.R <= a.E) tile = 4;
   else if (a.ids && a.R <= 2 * (int64_t)a.E) tile /= 2;
   if (tokens < tile) tile = tokens;
@@ -874,11 +900,11 @@ hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   // the second product, which holds the tokens in two parts (groups of 64, 2048:
   // 28.6 against 33.3; e2m1 22.7 against 24.2; groups of 128 26.8 against 26.4).
   const int steps = (a.K + kUnit - 1) / kUnit, last = steps % 4;
-  const int rounded = (steps + 3) / 4 * 4, row = parts<XE>() * tile * 2;
+  const int rounded = (steps + 3) / 4 * 4, row = parts<FMT, XE>() * tile * 2;
   // More LDS for the tokens, so that K fits whole, where all workgroups still
   // find a place at once (8 tokens of 4096 x 4096 in groups of 128: 7.7 us against
-  // 8.5, 16 tokens 10.3 against 11.3; 16 fp16 ones, which no longer do, 28.0
-  // against 19.3).
+  // 8.5, 16 tokens 10.3 against 11.3; 32 tokens of 4096 x 8192, which no longer
+  // do, 41.4 against 19.2).
   const int64_t whole = row * ((int64_t)rounded * kUnit + kPad);
   const int64_t groups = (int64_t)out_tiles<XE>(a) * grid_y(a, tile);
   int token_lds = kTokenLds;
