@@ -8,14 +8,17 @@
 // tokens leave the weights' bytes as the bound, so the weights are read once
 // per expert, straight from their plain row-major layout into registers, and
 // turned into bf16 there with about one instruction per weight:
-//   int4: (v & 0x000F000F) | 0x43004300 holds 128 + q of two nibbles, exactly.
-//         The group's sum of (128 + q) x minus (128 + z) times the group's sum
-//         of x, times s, is the group's part; both sums are fp32, the second
-//         one from the same matrix instruction with ones for weights (the
+//   int4: ((v << 3) & 0x00780078) | 0x41804180 holds 16 + q of two nibbles,
+//         exactly.  The group's sum of (16 + q) x minus (16 + z) times the
+//         group's sum of x, times s, is the group's part; both sums are fp32, the
+//         second one from the same matrix instruction with ones for weights (the
 //         vector units are the busier ones; sums taken once, as the tokens are
 //         brought into LDS, cost 8 tokens of 4096 x 4096 10.2 us against 9.0).
-//         The offset costs about five of fp32's 24 bits, against the 8 or 11 of
-//         the output.
+//         The offset costs about two of fp32's 24 bits: 16 is the smallest one
+//         that leaves the four bits of a code in one binade.  128, which saves the
+//         shift of every fourth pair, costs five and is no more than 2% faster
+//         (one token's FFN 22.7 us against 23.2, 32 tokens of 256 experts 397
+//         against 402).
 //         With fp16 activations the codes are fp16: 1024 + q in the same way,
 //         then 1032 taken off again, exactly, by a packed subtraction.  1024 + q
 //         itself, or q 2^-24 as a subnormal, would cost the matrix instruction's
@@ -95,7 +98,7 @@ __device__ __forceinline__ int buf_loadu16(__amdgpu_buffer_rsrc_t r, uint32_t vo
 // compiler takes an and and an or for each pair where one v_and_or does.
 template <bool HALF>
 struct Int4Bits {
-  uint32_t mask = 0x000F000Fu, bias = HALF ? 0x64006400u : 0x43004300u;
+  uint32_t mask = HALF ? 0x000F000Fu : 0x00780078u, bias = HALF ? 0x64006400u : 0x41804180u;
   __device__ __forceinline__ Int4Bits() { asm("" : "+s"(mask), "+v"(bias)); }
 };
 
@@ -110,14 +113,20 @@ __device__ __forceinline__ f32x4 mma(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// 8 int4 codes of one dword as bf16 128 + q or fp16 q - 8, in the order 0 4 1 5
+// 8 int4 codes of one dword as bf16 16 + q or fp16 q - 8, in the order 0 4 1 5
 // 2 6 3 7.
+constexpr float kInt4Offset = 16.f;
 template <bool HALF>
 __device__ __forceinline__ Operand<HALF> int4_operand(uint32_t v, const Int4Bits<HALF>& c) {
-  const uint4 b = make_uint4((v & c.mask) | c.bias, ((v >> 4) & c.mask) | c.bias,
-                             ((v >> 8) & c.mask) | c.bias, ((v >> 12) & c.mask) | c.bias);
-  if constexpr (HALF) return __builtin_bit_cast(f16x8, b) - (_Float16)1032.f;
-  else return __builtin_bit_cast(bf16x8, b);
+  if constexpr (HALF) {
+    const uint4 b = make_uint4((v & c.mask) | c.bias, ((v >> 4) & c.mask) | c.bias,
+                               ((v >> 8) & c.mask) | c.bias, ((v >> 12) & c.mask) | c.bias);
+    return __builtin_bit_cast(f16x8, b) - (_Float16)1032.f;
+  } else {
+    return __builtin_bit_cast(
+        bf16x8, make_uint4(((v << 3) & c.mask) | c.bias, ((v >> 1) & c.mask) | c.bias,
+                           ((v >> 5) & c.mask) | c.bias, ((v >> 9) & c.mask) | c.bias));
+  }
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -463,7 +472,7 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
   const bool has_zero = FMT == W4_INT && a.zero;
   const __amdgpu_buffer_rsrc_t rz = dword_rsrc(has_zero ? a.zero + (size_t)e * a.N * KG : a.w,
                                                has_zero ? (uint32_t)a.N * KG : 0, skip_z);
-  const float z0 = (HALF ? -8.f : 128.f) + (has_zero ? 0.f : 8.f);  // an empty buffer's loads read 0
+  const float z0 = (HALF ? -8.f : kInt4Offset) + (has_zero ? 0.f : 8.f);  // an empty buffer's loads read 0
   const bool one_scale = GM == 1 && FMT == W4_INT && KG == 1;  // of the whole row
 
   for (int m0 = 0; m0 < count; m0 += tile) {
@@ -699,7 +708,7 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
   const int KS = (a.K + 127) / 128, KG = a.K / a.group;
   const uint32_t pitch = (uint32_t)a.K / 2;
   const bool has_zero = FMT == W4_INT && a.zero;
-  const float z0 = has_zero ? 128.f : 136.f;
+  const float z0 = kInt4Offset + (has_zero ? 0.f : 8.f);
   const bool one_scale = GM == 1 && FMT == W4_INT && KG == 1;
   const Int4Bits<false> bits;
   float sum = 0.f;  // the product's rows all hold the token; the first is taken

@@ -12,9 +12,8 @@ in the low nibble.
 The error model is oracle.moe's for bf16 instructions: 32 products are added
 with a zero-mean error of standard deviation u times their 2-norm, and every
 fp32 addition and product rounds once, independently, u = 2^-24.  A whole-number
-weight is held as 128 + q and the group's (128 + z) sum(x) is taken off
-again, so both sums' errors scale with 143 (128 + 15), the largest weight
-held.
+weight is held as 16 + q and the group's (16 + z) sum(x) is taken off again,
+so both sums' errors scale with 31 (16 + 15), the largest weight held.
 Each function returns the value and one standard deviation of its error.
 """
 
@@ -23,7 +22,7 @@ import numpy as np
 from .codecs import e2m1_decode, e8m0_decode, fp4_unpack
 
 U = 2.0 ** -24
-LARGEST = 128.0 + 15.0
+LARGEST = 16.0 + 15.0
 
 
 def dequant(fmt, w, scale, zero, group):
