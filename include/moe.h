@@ -674,9 +674,8 @@ int moe_w4_matvec(int32_t format, int32_t elem, const void* x, int32_t x_per_rou
 
 /* The whole expert FFN: out[t] = sum_j topk_weights[t][j] * W2[e] . silu(gate)
  * * up, with gate, up = W1[e] . x[t], for the routes with e = topk_ids[t][j]
- * in [0, E); one rounding to elem at the end, the intermediate held as two
- * bf16 parts (16 significant bits).  w1 (E, N, K/2), w2
- * (E, K, N/4) bytes, N = 2I, with scales and zeros along K and I.  The
+ * in [0, E); one rounding to elem at the end, the intermediate held in the 24
+ * bits of fp32.  w1 (E, N, K/2), w2 (E, K, N/4) bytes, N = 2I, with scales and zeros along K and I.  The
  * workspace (device, 16-byte aligned, contents undefined on return; separate
  * for calls that may overlap) has at least moe_w4_workspace_size bytes. */
 int moe_w4_workspace_size(int64_t T, int64_t K, int64_t N, int32_t top_k, size_t* bytes);

@@ -60,6 +60,9 @@ int launched(hipError_t e) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+// The intermediate: three bf16 parts of R rows.
+size_t parts_bytes(size_t R, size_t I) { return R * I * 6; }
+
 }  // namespace
 
 extern "C" {
@@ -91,7 +94,7 @@ int moe_w4_workspace_size(int64_t T, int64_t K, int64_t N, int32_t top_k, size_t
   if (rc) return rc;
   if (N % 2) return abi_fail(MOE_ERR_SHAPE, "N (gate and up rows) must be even");
   const size_t R = (size_t)T * top_k;
-  *bytes = up256(R * (N / 2) * 4) + up256(R * K * 4);
+  *bytes = up256(parts_bytes(R, N / 2)) + up256(R * K * 4);
   return abi_ok();
 }
 
@@ -118,8 +121,8 @@ int fused_moe_w4(int32_t format, int32_t elem, const void* x, const void* w1, co
                     workspace ? workspace_bytes : (size_t)0, need);
   if (!aligned(workspace)) return abi_fail(MOE_ERR_ALIGN, "the workspace must be 16-byte aligned");
   const int R = (int)(T * top_k), I = (int)(N / 2);
-  void* h = workspace;  // (R, 2, I) bf16 parts
-  float* y = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256((size_t)R * I * 4));
+  void* h = workspace;  // (R, 3, I) bf16 parts
+  float* y = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256(parts_bytes(R, I)));
   hipStream_t s = static_cast<hipStream_t>(stream);
   W4Args up{x, static_cast<const uint8_t*>(w1), w1_scale, w1_zero, topk_ids, h,
             (int)K, (int)N, E, R, top_k, group ? group : (int)K,

@@ -43,8 +43,8 @@ hipError_t launch_route_backward(const int32_t* ids, const float* w, const float
 // 4-bit weights: formats in the order of moe_w4_format.
 enum : int { W4_INT = 0, W4_MX = 1 };
 
-// Rows of K values, each as two bf16 parts hi + lo: (2, K) in the order the
-// second product takes them.
+// Rows of K values, each as three bf16 parts p0 + p1 + 2 p2: (3, K) in the order
+// the second product takes them.
 constexpr int ELEM_PARTS = 4;
 
 // One set of products y[r] = W[e(r)] x[r or its token] with 4-bit weights.
@@ -64,7 +64,7 @@ struct W4Args {
 constexpr int kW4MaxRoutes = 4096;  // routes of one call (a workgroup lists its expert's)
 hipError_t launch_w4(int format, const W4Args& a, hipStream_t stream);
 // The second product of the FFN and the weighted sum: a.x the intermediate (R,
-// 2, K) in parts, a.out (T, N), out[t] = sum over t's routes with an expert in [0, E) of
+// 3, K) in parts, a.out (T, N), out[t] = sum over t's routes with an expert in [0, E) of
 // weights[r] W x[r].  y: R * N floats of workspace, unused at T <= kW4TokenMax.
 constexpr int kW4TokenMax = 4;
 hipError_t launch_w4_down(int format, const W4Args& a, const float* weights, float* y, int T,

@@ -29,8 +29,11 @@
 //         two is a bf16, so this is exact too.
 // Activations are operands as they are, except fp16 ones with e2m1 (whose scales
 // are out of fp16's range): two bf16 parts hi + lo, which is exact.  The FFN's
-// intermediate, an fp32 value, is written as two such parts (2^-17 of it is
-// lost), in the order the second product reads.
+// intermediate, an fp32 value, is written as three bf16 parts of eight bits each,
+// which is exact too, in the order the second product reads.  Its tokens (up to
+// eight) have two rows each in one instruction, a second instruction adds the
+// third part to both by halves, and the two rows are added at the end: as many
+// instructions as two parts would take.
 //
 // A 16x16x32 matrix instruction takes 16 tokens (A rows) and 16 weight rows (B
 // columns); a lane (n = l % 16, g = l / 16) reads 16 bytes of row n in each
@@ -71,10 +74,13 @@ constexpr int kUnit = kWaves * 128;     // K elements of one step of every wave
 constexpr int kPad = 8;                 // elements behind each token's row in LDS
 constexpr int kBlocks = 4;              // 64-route blocks found without a barrier
 // LDS of the tokens: a few tokens' whole K, or 1,024 elements of kTile tokens
-// (half as many of two parts); and the most that the sums and the list leave.
-constexpr int kTokenLds = kTile * (2 * kUnit + kPad) * 2;
+// (half as many of more parts); and the most that the sums and the list leave.
+template <int XE>
+constexpr int least_token_lds() {
+  return (XE == ELEM_PARTS ? kTile / 2 * 3 : kTile) * (2 * kUnit + kPad) * 2;
+}
 constexpr int kTokenLdsMost = 144 * 1024;
-constexpr int kSumLds = (kWaves - 1) * 2 * 1024;  // the waves' sums of two tiles
+constexpr int kSumLds = (kWaves - 1) * 2 * 1024;  // the waves' sums of two tiles, at most
 constexpr int kCUs = 256, kLds = 160 * 1024;      // of a CU
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -82,8 +88,11 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // fp16 activations stay fp16 where the codes can be fp16 too.
 template <int FMT, int XE>
 constexpr bool half_ops() { return FMT == W4_INT && XE == ELEM_F16; }
+// Operands of a product for each step of a token, and its rows in LDS.
 template <int FMT, int XE>
 constexpr int parts() { return XE == ELEM_BF16 || half_ops<FMT, XE>() ? 1 : 2; }
+template <int FMT, int XE>
+constexpr int lds_rows() { return XE == ELEM_PARTS ? 3 : parts<FMT, XE>(); }
 
 __device__ __forceinline__ float bits_to_f32(uint32_t u16, int elem) {
   return elem == ELEM_F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)u16)
@@ -156,7 +165,7 @@ __device__ __forceinline__ void transpose4(uint4& c) {
 // 8 consecutive activations of a lane: one 16-byte load, or one of each part.
 template <int XE>
 struct X8 {
-  uint4 v[XE == ELEM_PARTS ? 2 : 1];
+  uint4 v[XE == ELEM_PARTS ? 3 : 1];
 };
 
 // From k of a row of K.
@@ -164,7 +173,22 @@ template <int XE>
 __device__ __forceinline__ void load_tokens(X8<XE>& x, __amdgpu_buffer_rsrc_t r, uint32_t k,
                                             uint32_t K) {
   x.v[0] = buf_load16(r, k < K ? k * 2 : 0xFFFFFFF0u, 0);  // zeros past K
-  if constexpr (XE == ELEM_PARTS) x.v[1] = buf_load16(r, k < K ? (K + k) * 2 : 0xFFFFFFF0u, 0);
+  if constexpr (XE == ELEM_PARTS) {
+    x.v[1] = buf_load16(r, k < K ? (K + k) * 2 : 0xFFFFFFF0u, 0);
+    x.v[2] = buf_load16(r, k < K ? (2 * K + k) * 2 : 0xFFFFFFF0u, 0);
+  }
+}
+
+// The three parts of v that each lose nothing: v = p[0] + p[1] + 2 p[2], eight
+// bits a part (the last one halved, see above; below 2^-133 bits go).  An infinity
+// or NaN is whole in the first.
+__device__ __forceinline__ void split_parts(float v, uint16_t (&p)[3]) {
+  const uint32_t hi = __float_as_uint(v) & 0xFFFF0000u;
+  const float r = __builtin_isfinite(v) ? v - __uint_as_float(hi) : 0.f;
+  const uint32_t mid = __float_as_uint(r) & 0xFFFF0000u;
+  p[0] = (uint16_t)(hi >> 16);
+  p[1] = (uint16_t)(mid >> 16);
+  p[2] = (uint16_t)(__float_as_uint(0.5f * (r - __uint_as_float(mid))) >> 16);
 }
 
 // The place of element i of a row in the order that the weights' codes come in:
@@ -192,12 +216,13 @@ __device__ __forceinline__ float pair_sum(uint32_t d) {
   return __uint_as_float(d << 16) + __uint_as_float(d & 0xFFFF0000u);
 }
 
-// 8 activations into LDS as bf16 in that order, part 1 `part` elements after
-// part 0.  Returns their sum (int4 with bf16 operands; in fp32 as every sum here).
+// 8 activations into LDS as bf16 in that order, each part `part` elements after
+// the one before.  Returns their sum (int4 with bf16 operands; in fp32 as every sum
+// here).
 template <int FMT, int XE>
 __device__ __forceinline__ float store_tokens(const X8<XE>& x, uint16_t* to, int part) {
   const uint32_t d[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w};
-  uint32_t b[2][4];  // pairs of elements
+  uint32_t b[3][4];  // pairs of elements
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     b[0][i] = d[i], b[1][i] = 0;
@@ -209,11 +234,13 @@ __device__ __forceinline__ float store_tokens(const X8<XE>& x, uint16_t* to, int
                 (uint32_t)f32_to_bf16(h - __uint_as_float(h0 << 16)) << 16;
     }
   }
-  if constexpr (XE == ELEM_PARTS)  // in order already
+  if constexpr (XE == ELEM_PARTS) {  // in order already
     b[1][0] = x.v[1].x, b[1][1] = x.v[1].y, b[1][2] = x.v[1].z, b[1][3] = x.v[1].w;
+    b[2][0] = x.v[2].x, b[2][1] = x.v[2].y, b[2][2] = x.v[2].z, b[2][3] = x.v[2].w;
+  }
   float sum = 0.f;
 #pragma unroll
-  for (int p = 0; p < parts<FMT, XE>(); ++p) {
+  for (int p = 0; p < lds_rows<FMT, XE>(); ++p) {
     uint4 v = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
     if constexpr (FMT != W4_MX && XE != ELEM_PARTS)
       v = make_uint4(lo_halves(b[p][0], b[p][2]), hi_halves(b[p][0], b[p][2]),
@@ -221,7 +248,7 @@ __device__ __forceinline__ float store_tokens(const X8<XE>& x, uint16_t* to, int
     *reinterpret_cast<uint4*>(to + p * part) = v;
     if constexpr (FMT != W4_MX && !half_ops<FMT, XE>())
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum += pair_sum(b[p][i]);
+      for (int i = 0; i < 4; ++i) sum += (p == 2 ? 2.f : 1.f) * pair_sum(b[p][i]);
   }
   return sum;
 }
@@ -285,10 +312,10 @@ template <int FMT, int D, int GM, bool RAG>
 using ScaleWindow = Window<D * step_scales<FMT, GM>() * scale_bytes<FMT>(), RAG>;
 
 // acc[t] += tokens x weights of one 128-wide step, the u-th of its window.
-// xp: the lane's token at this step in LDS, the parts `part` elements apart.
-// valid: the scale groups of the step that the row has (RAG).  ONE: every row
-// of the product is the same token, whose sum over group q of the step is sx[q];
-// only the first row is made.  SE: type of int4 scales.
+// xp: the lane's row at this step in LDS, its P operands `part` elements apart.
+// valid: the scale groups of the step that the row has (RAG).  ONE: the product's
+// first four rows add up to one token, whose sum over group q of the step is
+// sx[q]; int4 adds them here, into the first.  SE: type of int4 scales.
 template <int FMT, int GM, bool RAG, int P, int NT, int D, bool ONE, int SE, bool HALF>
 __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* xp, int part,
                                              const float* sx,
@@ -324,15 +351,13 @@ __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* x
     }
   } else {
     constexpr int DG = 4 / GM;  // instructions of one group
-    f32x4 xsum[GM];
+    [[maybe_unused]] f32x4 xsum[GM];
+    if constexpr (!ONE) {
+      constexpr uint32_t one = HALF ? 0x3C003C00u : 0x3F803F80u;
+      const auto ones = __builtin_bit_cast(Operand<HALF>, make_uint4(one, one, one, one));
 #pragma unroll
-    for (int q = 0; q < GM; ++q) {
-      xsum[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if constexpr (ONE) {
-        xsum[q][0] = sx[q];
-      } else {
-        constexpr uint32_t one = HALF ? 0x3C003C00u : 0x3F803F80u;
-        const auto ones = __builtin_bit_cast(Operand<HALF>, make_uint4(one, one, one, one));
+      for (int q = 0; q < GM; ++q) {
+        xsum[q] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int d = q * DG; d < (q + 1) * DG; ++d)
 #pragma unroll
@@ -360,14 +385,25 @@ __device__ __forceinline__ void step_product(f32x4 (&acc)[NT], const uint16_t* x
         float s = bits_to_f32(RAG && one_scale ? sc[t].u16(0) : sc[t].u16(k), SE);
         const float z = z0 + (float)(RAG && one_scale ? zc[t].u8(0) : zc[t].u8(k));
         if (RAG && !one_scale && q >= valid) s = 0.f;  // past the row's end
+        if constexpr (ONE) {
+          acc[t][0] += s * ((v[0] + v[1]) + (v[2] + v[3]) - z * sx[q]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < (ONE ? 1 : 4); ++j) acc[t][j] += s * (v[j] - z * xsum[q][j]);
+          for (int j = 0; j < 4; ++j) acc[t][j] += s * (v[j] - z * xsum[q][j]);
+        }
       }
     }
   }
 }
 
 constexpr int kNone = (int)0x80000000;  // past every buffer
+
+// Lanes of a wave that hold sums (a token of three parts has two rows, the second
+// one in the upper half), and the LDS for the sums of all waves but the first.
+template <int XE>
+constexpr int sum_lanes() { return XE == ELEM_PARTS ? 32 : 64; }
+template <int XE, int NT>
+constexpr int sum_lds() { return (kWaves - 1) * NT * sum_lanes<XE>() * 16; }
 
 // GM: scale groups in a 128-wide step (int4: 1, 2, 4).  RAG: K is no multiple of
 // 512 or a row has one scale, so that the scales of D steps lie at any address,
@@ -379,15 +415,18 @@ constexpr int kNone = (int)0x80000000;  // past every buffer
 // routes without an expert here), or the block of `tile` tokens (no ids).
 template <int FMT, int XE, int SE, int GM, bool RAG, int NT, bool SWIGLU, int D>
 __global__ void
-__launch_bounds__(kThreads, GM > 1 ? 2 : NT == 2 && D == 4 && (RAG || parts<FMT, XE>() == 2) ? 3 : 4)
+__launch_bounds__(kThreads, XE == ELEM_PARTS ? (RAG && GM > 1 ? 2 : 3)
+                            : GM > 1 ? 2
+                            : NT == 2 && D == 4 && (RAG || parts<FMT, XE>() == 2) ? 3 : 4)
 k_w4(W4Args a, int tile, int run, int token_lds) {
-  constexpr int P = parts<FMT, XE>();
+  constexpr int P = parts<FMT, XE>(), PR = lds_rows<FMT, XE>();
   constexpr bool HALF = half_ops<FMT, XE>();
-  constexpr int kRowParts = XE == ELEM_PARTS ? 2 : 1;  // 16-bit rows of a token in memory
+  constexpr int kRowParts = XE == ELEM_PARTS ? 3 : 1;  // 16-bit rows of a token in memory
+  constexpr int kSumLanes = sum_lanes<XE>();
   extern __shared__ __align__(16) uint8_t smem[];
   uint16_t* xs = reinterpret_cast<uint16_t*>(smem);
   float* red = reinterpret_cast<float*>(smem + token_lds);  // waves 1.. of each tile
-  uint16_t* list = reinterpret_cast<uint16_t*>(smem + token_lds + (kWaves - 1) * NT * 1024);
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + token_lds + sum_lds<XE, NT>());
   __shared__ int wave_count[kWaves];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
@@ -478,11 +517,15 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
   for (int m0 = 0; m0 < count; m0 += tile) {
     const int nt = min(tile, count - m0);
     // steps of each wave in one part of K: what the LDS holds for nt tokens
-    const int fit = (token_lds / (P * nt * 2) - kPad) / kUnit;
+    const int fit = (token_lds / (PR * nt * 2) - kPad) / kUnit;
     const bool whole = D > 2 || fit >= JP;  // many steps ahead only where K fits
     const int S = whole ? JP : fit / D * D;  // fit >= D: the launch sees to it
     const int xrow = S * kUnit + kPad, inv_s = 65536 / S + 1;  // seg * inv_s >> 16 = seg / S
-    const uint16_t* xa = xs + (size_t)(n16 < nt ? n16 : 0) * xrow;
+    // the lane's row, and its second operand behind it; of three parts the first
+    // two are rows n16 and n16 + 8, the third is the second operand of both
+    const int lt = XE == ELEM_PARTS ? n16 & 7 : n16, lp = XE == ELEM_PARTS ? n16 >> 3 : 0;
+    const uint16_t* xa = xs + (size_t)(lp * nt + (lt < nt ? lt : 0)) * xrow;
+    const int part = (XE == ELEM_PARTS ? 2 - lp : 1) * nt * xrow;
 
     // Requests run D steps ahead of the products (the scales of a round of D
     // steps a round ahead of its weights), over the parts of K and the tiles in
@@ -567,8 +610,10 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
       }
     };
 
-    // tokens' elements in segments of 512, one a wave at a time
-    X8<XE> xr[2];
+    // tokens' elements in segments of 512, one a wave at a time, kAhead of them (a
+    // few loads either way) requested together
+    constexpr int kAhead = XE == ELEM_PARTS ? 1 : 2;
+    X8<XE> xr[kAhead];
     auto seg_request = [&](X8<XE>& x, int seg, int k0) {
       const int m = seg * inv_s >> 16;
       const bool on = m < nt;  // else an empty buffer
@@ -586,14 +631,14 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
     };
     auto stage = [&](int k0, bool begun) {
       const int segs = nt * S;
-      for (int seg = wave; seg < segs; seg += 2 * kWaves) {
+      for (int seg = wave; seg < segs; seg += kAhead * kWaves) {
         if (!begun) {
-          seg_request(xr[0], seg, k0);
-          seg_request(xr[1], seg + kWaves, k0);
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) seg_request(xr[i], seg + i * kWaves, k0);
         }
         begun = false;
-        seg_store(xr[0], seg);
-        seg_store(xr[1], seg + kWaves);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) seg_store(xr[i], seg + i * kWaves);
       }
     };
 
@@ -602,8 +647,8 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
 
     // the tokens' loads go first: loads return in order, so they are waited for
     // while the weights are still on their way
-    seg_request(xr[0], wave, 0);
-    seg_request(xr[1], wave + kWaves, 0);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) seg_request(xr[i], wave + i * kWaves, 0);
     scale_rows();
     scales_request();
     weight_rows();
@@ -617,10 +662,10 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
     for (int ti = tile0; ti < tile1; ++ti) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int part = 0; part < KS; part += S * kWaves) {
-        if (!whole && (part || ti > tile0)) {
+      for (int k0 = 0; k0 < KS; k0 += S * kWaves) {  // a part of K
+        if (!whole && (k0 || ti > tile0)) {
           __syncthreads();
-          stage(part * 128, false);
+          stage(k0 * 128, false);
           __syncthreads();
         }
         for (int i = 0; i < S; i += D) {
@@ -628,22 +673,31 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
           scales_request();
 #pragma unroll
           for (int u = 0; u < D; ++u) {
-            const int step = part + wave * S + i + u;
+            const int step = k0 + wave * S + i + u;
             if (step < KS)
               step_product<FMT, GM, RAG, P, NT, D, false, SE, HALF>(
-                  acc, xa + (wave * S + i + u) * 128, nt * xrow, nullptr, wq[u], sc, zc, u,
+                  acc, xa + (wave * S + i + u) * 128, part, nullptr, wq[u], sc, zc, u,
                   KG - step * SG, one_scale, z0, bits);
             weights_request(u);
           }
           if (next_round(pw)) weight_rows();
         }
       }
+      if constexpr (XE == ELEM_PARTS)  // a token's two rows
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t v = __float_as_uint(acc[t][j]);
+            const u32x2 h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+            acc[t][j] = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+          }
       // the waves' sums: the others' through LDS to the first, which writes
       if (wave) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           if (4 * g < nt)
-            *reinterpret_cast<f32x4*>(red + (((wave - 1) * NT + t) * 64 + lane) * 4) = acc[t];
+            *reinterpret_cast<f32x4*>(red + (((wave - 1) * NT + t) * kSumLanes + lane) * 4) = acc[t];
       }
       __syncthreads();
       if (wave == 0 && 4 * g < nt) {
@@ -651,7 +705,7 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int v = 0; v < kWaves - 1; ++v)
-            acc[t] += *reinterpret_cast<const f32x4*>(red + ((v * NT + t) * 64 + lane) * 4);
+            acc[t] += *reinterpret_cast<const f32x4*>(red + ((v * NT + t) * kSumLanes + lane) * 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int m = 4 * g + j;
@@ -663,10 +717,11 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
             const int n = ti * 16 + n16;
             if (n >= out_n) continue;
             if (a.oelem == ELEM_PARTS) {
-              uint16_t* row = static_cast<uint16_t*>(a.out) + (size_t)r * out_n * 2 + place_of<FMT>(n);
-              const uint32_t hi = f32_to_bf16(v);
-              row[0] = (uint16_t)hi;
-              row[out_n] = f32_to_bf16(v - __uint_as_float(hi << 16));
+              uint16_t* row = static_cast<uint16_t*>(a.out) + (size_t)r * out_n * 3 + place_of<FMT>(n);
+              uint16_t p[3];
+              split_parts(v, p);
+#pragma unroll
+              for (int i = 0; i < 3; ++i) row[(size_t)i * out_n] = p[i];
             } else {
               store_out(a.out, at, v, a.oelem);
             }
@@ -686,39 +741,44 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
 // 16 output columns of a token, and each wave one of the token's routes at a
 // time, over the whole of K.  Nothing goes through memory between the product
 // and the sum, and there is one launch less; an expert that two tokens chose is
-// read twice.  x (R, 2, K) in two parts.  Grid: x the columns, y the token.
+// read twice.  x (R, 3, K) in three parts: the product's first rows are those of
+// the token (the halved third one twice), so that one instruction does for all of
+// them.  Grid: x the columns, y the token.
 constexpr int kTokenWaves = 8;   // routes at once
 constexpr int kTokenPart = 2048; // K elements of a route in LDS at a time
+// elements from a part's row to the next: 80 bytes past the row, so that the three
+// parts' 16 bytes of the four lane groups (64 or 16 bytes apart) lie in different banks
+constexpr int kTokenRow = kTokenPart + 40;
 template <int FMT, int GM>
 constexpr int token_lds() {
-  return 2 * kTokenPart * 2 + (FMT == W4_INT ? kTokenPart / 128 * GM * 4 : 0);
+  return 3 * kTokenRow * 2 + (FMT == W4_INT ? kTokenPart / 128 * GM * 4 : 0);
 }
 
 template <int FMT, int SE, int GM, bool RAG>
 __global__ void __launch_bounds__(kTokenWaves * 64, 2)
 k_w4_token(W4Args a, const float* __restrict__ weights) {
-  constexpr int D = 8, P = 2, SB = scale_bytes<FMT>(), SG = step_scales<FMT, GM>();
-  constexpr int xrow = kTokenPart;  // every lane reads the same token: no padding
+  constexpr int D = 8, SB = scale_bytes<FMT>(), SG = step_scales<FMT, GM>();
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = wave_id(), waves = blockDim.x / 64;
   const int n16 = lane & 15, g = lane >> 4;
   const int t = blockIdx.y, n = min((int)blockIdx.x * 16 + n16, a.N - 1);
   uint16_t* xs = reinterpret_cast<uint16_t*>(smem + (size_t)wave * token_lds<FMT, GM>());
-  float* sums = reinterpret_cast<float*>(xs + P * xrow);  // of the scale groups
+  const uint16_t* xa = xs + min(n16, 2) * kTokenRow;
+  float* sums = reinterpret_cast<float*>(xs + 3 * kTokenRow);  // of the scale groups
   const int KS = (a.K + 127) / 128, KG = a.K / a.group;
   const uint32_t pitch = (uint32_t)a.K / 2;
   const bool has_zero = FMT == W4_INT && a.zero;
   const float z0 = kInt4Offset + (has_zero ? 0.f : 8.f);
   const bool one_scale = GM == 1 && FMT == W4_INT && KG == 1;
   const Int4Bits<false> bits;
-  float sum = 0.f;  // the product's rows all hold the token; the first is taken
+  float sum = 0.f;
 
   for (int q = wave; q < a.top_k; q += waves) {
     const int r = t * a.top_k + q;
     const int e = a.ids[r];
     if ((unsigned)e >= (unsigned)a.E) continue;
     const __amdgpu_buffer_rsrc_t rx =
-        make_rsrc(static_cast<const uint16_t*>(a.x) + (size_t)r * a.K * 2, (uint32_t)a.K * 4);
+        make_rsrc(static_cast<const uint16_t*>(a.x) + (size_t)r * a.K * 3, (uint32_t)a.K * 6);
     const __amdgpu_buffer_rsrc_t rw =
         make_rsrc(a.w + (size_t)e * a.N * pitch, (uint32_t)a.N * pitch);
     int skip_s, skip_z;
@@ -760,7 +820,7 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
 #pragma unroll
       for (int i = 0; i < kTokenPart / 512; ++i)
       {
-        float v = store_tokens<FMT, ELEM_PARTS>(xr[i], xs + i * 512 + lane * 8, xrow);
+        float v = store_tokens<FMT, ELEM_PARTS>(xr[i], xs + i * 512 + lane * 8, kTokenRow);
         if constexpr (FMT == W4_INT) {
           v = group_sum<GM>(v);
           if (lane % (16 / GM) == 0) sums[(i * 512 + lane * 8) / (128 / GM)] = v;
@@ -779,15 +839,15 @@ k_w4_token(W4Args a, const float* __restrict__ weights) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
           if (s0 + u < KS)
-            step_product<FMT, GM, RAG, P, 1, D, true, SE, false>(
-                acc, xs + (s0 + u) * 128 - k0, xrow, sums + ((s0 + u) - k0 / 128) * GM, wq[u], sc,
+            step_product<FMT, GM, RAG, 1, 1, D, true, SE, false>(
+                acc, xa + (s0 + u) * 128 - k0, 0, sums + ((s0 + u) - k0 / 128) * GM, wq[u], sc,
                 zc, u, KG - (s0 + u) * SG, one_scale, z0, bits);
           weights_request(u, s0 + u + D);
         }
       }
       wave_lds_fence();
     }
-    sum += weights[r] * acc[0][0];
+    sum += weights[r] * (FMT == W4_MX ? (acc[0][0] + acc[0][1]) + (acc[0][2] + acc[0][3]) : acc[0][0]);
   }
   float* red = reinterpret_cast<float*>(smem);
   __syncthreads();  // the tokens are read
@@ -866,7 +926,7 @@ hipError_t launch_one(const W4Args& a, int tile, int token_lds, hipStream_t stre
   // several tiles a workgroup once there are more workgroups than the GPU holds
   const int64_t all = (int64_t)tiles * y;
   const int run = all < 4096 ? 1 : all < 8192 ? 2 : 4;
-  const int lds = token_lds + (kWaves - 1) * NT * 1024 + list_bytes(a);
+  const int lds = token_lds + sum_lds<XE, NT>() + list_bytes(a);
   constexpr auto kernel = k_w4<FMT, XE, SE, GM, RAG, NT, SWIGLU, D>;
   if (lds > 65536) {
     const hipError_t e = allow_lds<kernel>(kTokenLdsMost + kSumLds + kW4MaxRoutes * 2);
@@ -890,7 +950,7 @@ hipError_t launch_shape(const W4Args& a, int tile, int token_lds, hipStream_t st
 
 template <int FMT, int XE, int SE, int GM, bool RAG>
 hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
-  // Tokens of one pass over the weights: 16, or 8 of two parts, so that two
+  // Tokens of one pass over the weights: 16, or 8 of more parts, so that two
   // steps of them fit the LDS.  Where the experts have few routes on average,
   // passes of fewer tokens leave room for more steps ahead, and an expert with
   // more routes takes another pass (T = 32, 256 experts, top-6: 369 us with
@@ -905,23 +965,25 @@ hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   // others: two is better there (40 routes of 64 experts, groups of 128, first
   // product: K = 1024 17.5 us against 20.2, 2048 38.1 against 35.4).  Narrow groups
   // are short of vector instructions before they are short of loads in flight
-  // (groups of 32, 2048: 43.4 against 49.0; 4096: 83.3 against 81.2), and so is
-  // the second product, which holds the tokens in two parts (groups of 64, 2048:
-  // 28.6 against 33.3; e2m1 22.7 against 24.2; groups of 128 26.8 against 26.4).
+  // (groups of 32, 2048: 43.4 against 49.0; 4096: 83.3 against 81.2), and so are
+  // those of 64 in the second product, which holds the tokens in three parts (FFN
+  // of 8 tokens, 256 experts, top-6, K = 1024, I = 2048: 54.1 us with two steps,
+  // 54.6 with four; I = 1920 52.9 and 56.4; e2m1 49.2 and 49.2, 32 tokens 121.5
+  // and 120.1).
   const int steps = (a.K + kUnit - 1) / kUnit, last = steps % 4;
-  const int rounded = (steps + 3) / 4 * 4, row = parts<FMT, XE>() * tile * 2;
+  const int rounded = (steps + 3) / 4 * 4, row = lds_rows<FMT, XE>() * tile * 2;
   // More LDS for the tokens, so that K fits whole, where all workgroups still
   // find a place at once (8 tokens of 4096 x 4096 in groups of 128: 7.7 us against
   // 8.5, 16 tokens 10.3 against 11.3; 32 tokens of 4096 x 8192, which no longer
   // do, 41.4 against 19.2).
   const int64_t whole = row * ((int64_t)rounded * kUnit + kPad);
   const int64_t groups = (int64_t)out_tiles<XE>(a) * grid_y(a, tile);
-  int token_lds = kTokenLds;
-  if (whole > kTokenLds && whole <= kTokenLdsMost &&
+  int token_lds = least_token_lds<XE>();
+  if (whole > token_lds && whole <= kTokenLdsMost &&
       groups <= kCUs * (kLds / (whole + kSumLds + list_bytes(a) + 64)))
     token_lds = (int)(whole + 15) / 16 * 16;
   const int held = (token_lds / row - kPad) / kUnit;
-  if constexpr (XE != ELEM_PARTS || (FMT == W4_INT && GM == 1)) {
+  if constexpr (XE != ELEM_PARTS || GM == 1) {
     if (held >= rounded && (last == 0 || last == 3) && (GM < 4 || steps > 6))
       return launch_shape<FMT, XE, SE, GM, RAG, true>(a, tile, token_lds, stream);
   }

@@ -39,7 +39,7 @@ def dequant(fmt, w, scale, zero, group):
 
 def product(fmt, w, scale, zero, group, x, parts):
     """y = W x for one row x: (y, sigma), both (N,).  ``parts``: bf16 operands
-    a value of x is held as (fp32 values in two parts keep 2^-17 of each)."""
+    a value of x is held as, each an addition of its own."""
     W = dequant(fmt, w, scale, zero, group)
     x = np.asarray(x, np.float64)
     with np.errstate(invalid="ignore"):
@@ -93,8 +93,7 @@ def ffn(fmt, W1, W2, group, x, ids, weights, parts):
             h, sh = silu_mul((y[:I], s[:I]), (y[I:], s[I:]))
             y, s = product(fmt, *two, g2, h, 2)
             d = dequant(fmt, *two, g2)
-            # what comes in with h, and its two bf16 parts
-            s2 = s ** 2 + (d * d) @ (sh ** 2 + (2.0 ** -17 * h) ** 2)
+            s2 = s ** 2 + (d * d) @ sh ** 2  # and what comes in with h
             w = float(weights[t, j])
             out[t] += w * y
             var[t] += w * w * s2
