@@ -405,6 +405,8 @@ constexpr int sum_lanes() { return XE == ELEM_PARTS ? 32 : 64; }
 template <int XE, int NT>
 constexpr int sum_lds() { return (kWaves - 1) * NT * sum_lanes<XE>() * 16; }
 
+// The bound on waves keeps every instantiation out of scratch memory, whose
+// accesses the waits for the requested steps would count too.
 // GM: scale groups in a 128-wide step (int4: 1, 2, 4).  RAG: K is no multiple of
 // 512 or a row has one scale, so that the scales of D steps lie at any address,
 // and a row may end inside a step.  NT: 16-row weight tiles taken together; with
@@ -415,7 +417,7 @@ constexpr int sum_lds() { return (kWaves - 1) * NT * sum_lanes<XE>() * 16; }
 // routes without an expert here), or the block of `tile` tokens (no ids).
 template <int FMT, int XE, int SE, int GM, bool RAG, int NT, bool SWIGLU, int D>
 __global__ void
-__launch_bounds__(kThreads, XE == ELEM_PARTS ? (RAG && GM > 1 ? 2 : 3)
+__launch_bounds__(kThreads, XE == ELEM_PARTS ? (RAG && GM == 4 ? 2 : 3)
                             : GM > 1 ? 2
                             : NT == 2 && D == 4 && (RAG || parts<FMT, XE>() == 2) ? 3 : 4)
 k_w4(W4Args a, int tile, int run, int token_lds) {
@@ -536,11 +538,14 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
     ScaleWindow<FMT, D, GM, RAG> sn[NT], sc[NT];  // the next round's scales, this one's
     ZeroWindow<D, GM, RAG> zn[NT], zc[NT];
     constexpr bool ZRAG = RAG || D * GM % 4 != 0;
-    int wrow[NT], srow[NT], zrow[NT];
+    // the places of a tile's rows (an up row's follows from the gate's, a zero
+    // point's from its scale's: registers are short)
+    constexpr int NR = SWIGLU ? 1 : NT;
+    int wrow[NR], srow[NR];
     auto weight_row = [&](int t0, int t) {
-      return SWIGLU ? t * out_n + min(t0 * 16 + n16, out_n - 1)
-                    : min((t0 * NT + t) * 16 + n16, a.N - 1);
+      return SWIGLU ? min(t0 * 16 + n16, out_n - 1) : min((t0 * NT + t) * 16 + n16, a.N - 1);
     };
+    const int up_rows = SWIGLU ? out_n : 0;
     // a position in the walk: tile, part of K, round's first step in the part
     struct Pos {
       int tile, part, i;
@@ -558,15 +563,14 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
     };
     auto weight_rows = [&] {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NR; ++t)
         wrow[t] = pw.tile < tile1 ? (int)((uint32_t)weight_row(pw.tile, t) * pitch + 16 * g) : kNone;
     };
     auto scale_rows = [&] {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int t = 0; t < NR; ++t) {
         const int n = weight_row(ps.tile, t) * KG;
         srow[t] = ps.tile < tile1 ? n * SB + skip_s : kNone;
-        zrow[t] = ps.tile < tile1 ? n + skip_z : kNone;
       }
     };
     auto weights_request = [&](int u) {
@@ -575,8 +579,9 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
       for (int t = 0; t < NT; ++t) {
         // where a row may end inside a step, the whole offset is the one that the
         // range check sees
-        const int at = RAG && wrow[t] != kNone ? wrow[t] + step * 64 : wrow[t];
-        wq[u][t] = buf_load16(rw, (uint32_t)at, RAG ? 0 : (uint32_t)step * 64);
+        const int row = wrow[t % NR];
+        const uint32_t at = (RAG && row != kNone ? row + step * 64 : row) + t * up_rows * pitch;
+        wq[u][t] = buf_load16(rw, at, RAG ? 0 : (uint32_t)step * 64);
       }
     };
     auto scale_step = [&](const Pos& p) {
@@ -588,9 +593,12 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
       const int c = scale_step(ps) * SG;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const bool on = srow[t] != kNone;
-        const int so = RAG && on ? srow[t] + c * SB : srow[t];
-        const int zo = ZRAG && on ? zrow[t] + c : zrow[t];
+        const int row = srow[t % NR];
+        const bool on = row != kNone;
+        const int srow_t = on ? row + t * up_rows * KG * SB : kNone;
+        const int so = RAG && on ? srow_t + c * SB : srow_t;
+        const int zrow = on ? (srow_t - skip_s) / SB + skip_z : kNone;
+        const int zo = ZRAG && on ? zrow + c : zrow;
         sn[t].load(rs, so, RAG ? 0 : c * SB);
         if constexpr (FMT == W4_INT) zn[t].load(rz, zo, ZRAG ? 0 : c);
         salign[t] = so;
@@ -969,7 +977,8 @@ hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   // those of 64 in the second product, which holds the tokens in three parts (FFN
   // of 8 tokens, 256 experts, top-6, K = 1024, I = 2048: 54.1 us with two steps,
   // 54.6 with four; I = 1920 52.9 and 56.4; e2m1 49.2 and 49.2, 32 tokens 121.5
-  // and 120.1).
+  // and 120.1).  Its ragged int4 rows of 128 have registers for two only, of three
+  // waves a SIMD (I = 1920: 51.5 us against 52.5 with four, which spill).
   const int steps = (a.K + kUnit - 1) / kUnit, last = steps % 4;
   const int rounded = (steps + 3) / 4 * 4, row = lds_rows<FMT, XE>() * tile * 2;
   // More LDS for the tokens, so that K fits whole, where all workgroups still
@@ -983,7 +992,7 @@ hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
       groups <= kCUs * (kLds / (whole + kSumLds + list_bytes(a) + 64)))
     token_lds = (int)(whole + 15) / 16 * 16;
   const int held = (token_lds / row - kPad) / kUnit;
-  if constexpr (XE != ELEM_PARTS || GM == 1) {
+  if constexpr (XE != ELEM_PARTS || (GM == 1 && !(RAG && FMT == W4_INT))) {
     if (held >= rounded && (last == 0 || last == 3) && (GM < 4 || steps > 6))
       return launch_shape<FMT, XE, SE, GM, RAG, true>(a, tile, token_lds, stream);
   }
