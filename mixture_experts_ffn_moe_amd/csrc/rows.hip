@@ -386,9 +386,14 @@ k_route_backward(const int32_t* __restrict__ ids, const float* __restrict__ w,
 
 // Whether the routes' rows are streamed past the caches: once they outgrow the
 // 256 MiB memory-side cache.  Measured at K = 4096, top-8 (permute, then
-// unpermute): 8,192 tokens (537 MB) 220 us streamed against 262, 4,096 tokens
-// 113 against 134; 2,048 tokens (134 MB), whose rows the second call finds in the
+// unpermute): 8,192 tokens (537 MB) 225 us streamed against 264, 4,096 tokens
+// 119 against 145; 2,048 tokens (134 MB), whose rows the second call finds in the
 // cache, 61 against 56, and 64 tokens 29 against 23.
+// Every route counts as placed, since the host does not know how many are.  Three
+// quarters of them elsewhere, the same calls and the weighted sum's gradient:
+// 4,096 tokens (67 MB placed) 46 us streamed against 44 and 41 against 33, 8,192
+// tokens (133 MB) 82 against 81 and 74 against 79, 16,384 156 against 172 and 145
+// against 158.
 bool streams(const RowsArgs& a, int64_t pitch) {
   return a.T * (a.top_k + a.n_shared) * pitch > (int64_t(192) << 20);
 }
@@ -399,8 +404,9 @@ int col_blocks(int64_t pitch, int es) {
 }
 
 // Runs f<alignment of a row's vectors, STREAM>: 16 bytes where the pitch keeps
-// it, else the element's (A < 16, never streamed: such rows are short of the
-// bandwidth where that matters).
+// it, else the element's (A < 16, never streamed.  8,192 tokens, top-8, bf16,
+// permute and unpermute: K = 4100 282 us streamed against 280, K = 4099 300
+// against 281; 2,048 tokens 113 against 88 and 119 against 92).
 template <int ES, class F>
 hipError_t by_pitch(const RowsArgs& a, int64_t pitch, F f) {
   typedef std::integral_constant<int, 16> whole;
