@@ -13,7 +13,8 @@ The error model is oracle.moe's for bf16 instructions: 32 products are added
 with a zero-mean error of standard deviation u times their 2-norm, and every
 fp32 addition and product rounds once, independently, u = 2^-24.  A whole-number
 weight is held as 16 + q and the group's (16 + z) sum(x) is taken off again,
-so both sums' errors scale with 31 (16 + 15), the largest weight held.
+so both sums' errors scale with 31 (16 + 15), the largest weight held; beside
+fp16 activations it is held as q - 8, and that largest one is 8.
 Each function returns the value and one standard deviation of its error.
 """
 
@@ -23,6 +24,14 @@ from .codecs import e2m1_decode, e8m0_decode, fp4_unpack
 
 U = 2.0 ** -24
 LARGEST = 16.0 + 15.0
+
+
+def operands(fmt, elem):
+    """(operands an activation of type ``elem`` is held as, largest whole-number
+    weight held beside it)."""
+    if elem == "f16":
+        return (1, 8.0) if fmt == "int4" else (2, None)
+    return 1, LARGEST
 
 
 def dequant(fmt, w, scale, zero, group):
@@ -37,9 +46,10 @@ def dequant(fmt, w, scale, zero, group):
     return ((q - z) * s).reshape(len(q), -1)
 
 
-def product(fmt, w, scale, zero, group, x, parts):
+def product(fmt, w, scale, zero, group, x, parts, largest=LARGEST):
     """y = W x for one row x: (y, sigma), both (N,).  ``parts``: bf16 operands
-    a value of x is held as, each an addition of its own."""
+    a value of x is held as, each an addition of its own; ``largest``: whole-number
+    weight held (see operands)."""
     W = dequant(fmt, w, scale, zero, group)
     x = np.asarray(x, np.float64)
     with np.errstate(invalid="ignore"):
@@ -49,14 +59,14 @@ def product(fmt, w, scale, zero, group, x, parts):
     span = np.abs(y) + 3 * np.sqrt(terms2)
     # the running sum: one addition per group (per 32 for the microscaling
     # format, where the instruction adds), its product with the scale, and
-    # the sums of eight waves
+    # the waves' sums
     steps = (W.shape[1] // 32 if fmt == "mx" else n) * parts
     var = U * U * (terms2 + (steps + 12) * span ** 2)
     if fmt != "mx":
         xg = x.reshape(n, group)
         q = (xg * xg).sum(1)
         run = np.abs(xg.sum(1)) + 3 * np.sqrt(q)
-        in_group = LARGEST ** 2 * (q + (group // 32 * parts + 2) * run ** 2)
+        in_group = largest ** 2 * (q + (group // 32 * parts + 2) * run ** 2)
         var = var + 2 * U * U * (np.asarray(scale, np.float64) ** 2) @ in_group
     return y, np.sqrt(var)
 

@@ -1,14 +1,19 @@
 """What the products with 4-bit weights keep of their sums and of the FFN's
 intermediate: results that are small differences of large terms.
 
-Every value below is a whole multiple of a power of two, and every sum that
-fp32 and the documented operands need stays below 2^24 of that power, so each
-result is exact."""
+Where nothing else is said every value is a whole multiple of a power of two, and
+every sum that fp32 and the documented operands need stays below 2^24 of that
+power, so each result is exact."""
 
+import numpy as np
 import pytest
 import torch
 
 import mixture_experts_ffn_moe_amd as moe
+from oracle import w4
+
+from .test_gpu_w4 import check
+from .test_oracle_w4_types import cancelling
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +123,16 @@ def test_intermediate_near_the_largest(T):
     got = moe.fused_moe_w4("mx", x.bfloat16().cuda(), *W1, *W2, ids, w, 32).cpu().float()
     assert bool((got[:, 0] == 2.0 ** 108).all())        # 511 / 256 2^107, rounded to bf16
     assert not bool(got[:, 1:].any())
+
+
+@pytest.mark.parametrize("group,zeros", [(128, False), (128, True), (64, True), (32, True)])
+@pytest.mark.parametrize("T", [1, 5, 19])
+def test_fp16_sums_of_large_terms(T, group, zeros):
+    """Within six deviations of the error model for codes held as q - 8."""
+    rng = np.random.default_rng(T + group)
+    w, s, z, x = cancelling(group, zeros, 48, 512, T, rng)
+    dev = [torch.from_numpy(w)[None].cuda(), torch.from_numpy(s).half()[None].cuda(),
+           None if z is None else torch.from_numpy(z)[None].cuda()]
+    got = moe.moe_w4_matvec("int4", torch.from_numpy(x).half().cuda(), *dev, None, group)
+    ref = [w4.product("int4", w, s, z, group, v, *w4.operands("int4", "f16")) for v in x]
+    check(got, np.stack([y for y, _ in ref]), np.stack([d for _, d in ref]), "f16", "large terms")
