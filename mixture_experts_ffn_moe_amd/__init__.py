@@ -556,6 +556,17 @@ def _output(out, name, shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _outside_autograd(*tensors):
+    """The calls on a plan's rows are steps of a torch.autograd.Function, not
+    nodes of a graph themselves: an input whose gradient would silently stop
+    there is refused."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise MoeError(-3, "an input requires a gradient that autograd would lose here: make the "
+                               "call inside a torch.autograd.Function (its backward is the entry "
+                               "point of that name) or under torch.no_grad()")
+
+
 def _enqueue(fn, dev, stream, *args):
     """Calls an entry point on the tensors' device: on its current stream, or on ``stream``."""
     if stream is None:
@@ -607,7 +618,10 @@ def moe_permute(x, row_of_route, sorted_token_ids, num_tokens_post_padded, top_k
     """Tokens (T, K) into the rows of a plan: (len(sorted_token_ids), K), each
     routed token in its routes' rows, zeros in the padding rows.  Rows at or
     past num_tokens_post_padded are left as they are (unspecified in a new
-    tensor).  x: bf16, fp16, fp32, or one-byte values (e4m3, scales)."""
+    tensor).  x: bf16, fp16, fp32, or one-byte values (e4m3, scales).
+    This call and the four below are made to be the steps of a
+    torch.autograd.Function; with gradients enabled they refuse inputs that
+    require one."""
     T, K = _matrix(x, "x")
     dev = x.device
     elem = _elem(x, "x")
@@ -617,6 +631,7 @@ def moe_permute(x, row_of_route, sorted_token_ids, num_tokens_post_padded, top_k
     plan = _operand(sorted_token_ids, "sorted_token_ids", torch.int32, (cap,), dev)
     ntp = _operand(num_tokens_post_padded, "num_tokens_post_padded", torch.int32, (1,), dev)
     out = _output(out, "out", (cap, K), x.dtype, dev, stream)
+    _outside_autograd(x)
     _enqueue(lib().moe_permute, dev, stream, elem, xp, row, plan, ntp, out.data_ptr(), T, K, top_k,
              n_shared, cap)
     return out
@@ -632,6 +647,7 @@ def moe_permute_backward(d_rows, row_of_route, top_k, n_shared=0, stream=None, o
     g = _operand(d_rows, "d_rows", d_rows.dtype, (cap, K), dev)
     row = _operand(row_of_route, "row_of_route", torch.int32, (n,), dev)
     out = _output(out, "out", (T, K), d_rows.dtype, dev, stream)
+    _outside_autograd(d_rows)
     _enqueue(lib().moe_permute_backward, dev, stream, elem, g, row, out.data_ptr(), T, K, top_k,
              n_shared, cap)
     return out
@@ -653,6 +669,7 @@ def moe_unpermute(rows, row_of_route, topk_weights, top_k, n_shared=0, stream=No
     w = None if topk_weights is None else _operand(topk_weights, "topk_weights", torch.float32,
                                                    (T, top_k), dev)
     out = _output(out, "out", (T, K), rows.dtype, dev, stream)
+    _outside_autograd(rows, topk_weights)
     _enqueue(lib().moe_unpermute, dev, stream, elem, y, row, w, out.data_ptr(), T, K, top_k,
              n_shared, cap)
     return out
@@ -680,6 +697,7 @@ def moe_unpermute_backward(d_out, rows, row_of_route, sorted_token_ids, num_toke
     d_rows = _output(d_rows, "d_rows", (cap, K), d_out.dtype, dev, stream)
     d_w = None if rows is None else _output(d_w, "d_weights", (T, top_k), torch.float32, dev,
                                             stream)
+    _outside_autograd(d_out, rows, topk_weights)
     _enqueue(lib().moe_unpermute_backward, dev, stream, elem, g, y, row, plan, ntp, w,
              d_rows.data_ptr(), None if d_w is None else d_w.data_ptr(), T, K, top_k, n_shared,
              cap)
@@ -699,6 +717,7 @@ def moe_route_backward(topk_ids, topk_weights, d_weights, num_experts, stream=No
     if num_experts < 1:
         raise MoeError(-2, f"num_experts must be >= 1 (got {num_experts})")
     out = _output(out, "out", (T, num_experts), torch.float32, dev, stream)
+    _outside_autograd(topk_weights, d_weights)
     _enqueue(lib().moe_route_backward, dev, stream, ids, w, d, out.data_ptr(), T, num_experts, k)
     return out
 
