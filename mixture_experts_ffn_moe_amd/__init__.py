@@ -593,6 +593,12 @@ def _routes(n, top_k, n_shared):
     return n // per
 
 
+def _experts(n):
+    """Refuses expert counts that the C ABI's int32 would not hold as they are."""
+    if not 1 <= n < 1 << 31:
+        raise MoeError(-2, f"num_experts must be in [1, 2^31) (got {n})")
+
+
 def moe_route_rows(topk_ids, num_experts, sorted_token_ids, num_tokens_post_padded, n_shared=0,
                    stream=None, out=None):
     """The inverse of a plan: (T * (top_k + n_shared)) int32, the row of each
@@ -603,6 +609,7 @@ def moe_route_rows(topk_ids, num_experts, sorted_token_ids, num_tokens_post_padd
     _on_gpu(topk_ids, "topk_ids")
     if n_shared < 0:
         raise MoeError(-2, f"n_shared must be >= 0 (got {n_shared})")
+    _experts(num_experts)
     cap = sorted_token_ids.numel()
     ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
     plan = _operand(sorted_token_ids, "sorted_token_ids", torch.int32, (cap,), dev)
@@ -714,8 +721,7 @@ def moe_route_backward(topk_ids, topk_weights, d_weights, num_experts, stream=No
     ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
     w = _operand(topk_weights, "topk_weights", torch.float32, (T, k), dev)
     d = _operand(d_weights, "d_weights", torch.float32, (T, k), dev)
-    if num_experts < 1:
-        raise MoeError(-2, f"num_experts must be >= 1 (got {num_experts})")
+    _experts(num_experts)
     out = _output(out, "out", (T, num_experts), torch.float32, dev, stream)
     _outside_autograd(topk_weights, d_weights)
     _enqueue(lib().moe_route_backward, dev, stream, ids, w, d, out.data_ptr(), T, num_experts, k)
