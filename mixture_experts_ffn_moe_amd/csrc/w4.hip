@@ -99,10 +99,6 @@ __device__ __forceinline__ float bits_to_f32(uint32_t u16, int elem) {
                           : __uint_as_float(u16 << 16);
 }
 
-__device__ __forceinline__ int buf_loadu16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
-  return (int)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)voff, (int)soff, 0);
-}
-
 // The two constants of the int4 conversion, in registers: as literals the
 // compiler takes an and and an or for each pair where one v_and_or does.
 template <bool HALF>
