@@ -2,12 +2,9 @@
 // (moe_route_rows, moe_permute, moe_unpermute and their gradients) and of the
 // router's gradient: argument checks before anything is enqueued, then the
 // launch.
-#include "../../include/moe.h"
-#include "ops.h"
+#include "abi_checks.h"
 
 namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // workgroups of 256 threads in one launch: the grid's thread count is 32-bit
 constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
@@ -36,31 +33,11 @@ int check_rows(int32_t elem, int64_t T, int64_t K, int32_t top_k, int32_t n_shar
   return MOE_OK;
 }
 
-struct Ptr {
-  const void* p;
-  bool needed;
-};
-
-template <size_t N>
-int check_ptrs(const Ptr (&ps)[N]) {
-  for (const Ptr& q : ps)
-    if (q.needed && !q.p) return abi_fail(MOE_ERR_NULL, "a required pointer is NULL");
-  for (const Ptr& q : ps)
-    if (q.p && !aligned(q.p, 16))
-      return abi_fail(MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
-  return MOE_OK;
-}
-
 int check_ntp(const int32_t* ntp) {
   if (!ntp) return abi_fail(MOE_ERR_NULL, "num_tokens_post_padded is NULL");
   if (!aligned(ntp, 4))
     return abi_fail(MOE_ERR_ALIGN, "num_tokens_post_padded must be 4-byte aligned");
   return MOE_OK;
-}
-
-int launched(hipError_t e) {
-  return e == hipSuccess ? abi_ok()
-                         : abi_fail(MOE_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
 }
 
 }  // namespace

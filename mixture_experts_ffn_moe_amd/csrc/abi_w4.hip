@@ -1,12 +1,9 @@
 // abi_w4.hip -- host side of the C ABI's products with 4-bit weights
 // (moe_w4_matvec, fused_moe_w4): argument checks before anything is enqueued,
 // workspace layout, launches.
-#include "../../include/moe.h"
-#include "ops.h"
+#include "abi_checks.h"
 
 namespace {
-
-bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
 
 int check_sizes(int32_t format, int32_t elem, int64_t T, int64_t K, int64_t N, int32_t E,
                 int32_t top_k, int64_t group) {
@@ -37,25 +34,6 @@ int check_group(int32_t format, int64_t L, int64_t group) {
     return abi_fail(MOE_ERR_UNSUPPORTED, "the contraction (%lld) must be a multiple of %lld",
                     (long long)L, (long long)unit);
   return MOE_OK;
-}
-
-struct Ptr {
-  const void* p;
-  bool needed;
-};
-
-template <size_t N>
-int check_ptrs(const Ptr (&ps)[N]) {
-  for (const Ptr& q : ps)
-    if (q.needed && !q.p) return abi_fail(MOE_ERR_NULL, "a required pointer is NULL");
-  for (const Ptr& q : ps)
-    if (q.p && !aligned(q.p)) return abi_fail(MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
-  return MOE_OK;
-}
-
-int launched(hipError_t e) {
-  return e == hipSuccess ? abi_ok()
-                         : abi_fail(MOE_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
