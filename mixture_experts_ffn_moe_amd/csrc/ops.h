@@ -65,7 +65,8 @@ constexpr int kW4MaxRoutes = 4096;  // routes of one call (a workgroup lists its
 hipError_t launch_w4(int format, const W4Args& a, hipStream_t stream);
 // The second product of the FFN and the weighted sum: a.x the intermediate (R,
 // 3, K) in parts, a.out (T, N), out[t] = sum over t's routes with an expert in [0, E) of
-// weights[r] W x[r].  y: R * N floats of workspace, unused at T <= kW4TokenMax.
+// weights[r] W x[r].  y: R * N floats of workspace.  Up to kW4TokenMax tokens can
+// take the kernel of a route per wave, which leaves y alone.
 constexpr int kW4TokenMax = 4;
 hipError_t launch_w4_down(int format, const W4Args& a, const float* weights, float* y, int T,
                           hipStream_t stream);

@@ -741,7 +741,7 @@ k_w4(W4Args a, int tile, int run, int token_lds) {
   }
 }
 
-// The second product and the weighted sum of one token at once: a workgroup has
+// The second product and the weighted sum of a token at once: a workgroup has
 // 16 output columns of a token, and each wave one of the token's routes at a
 // time, over the whole of K.  Nothing goes through memory between the product
 // and the sum, and there is one launch less; an expert that two tokens chose is
@@ -1056,10 +1056,15 @@ hipError_t launch_token_int4(const W4Args& a, const float* weights, int T, hipSt
 
 hipError_t launch_w4_down(int format, const W4Args& a, const float* weights, float* y, int T,
                           hipStream_t stream) {
-  // Few tokens' routes seldom share an expert, so its weights are read once
-  // either way (mx, 256 experts, top-6: 40.0 us against 44.0 for two tokens, 75
-  // against 75 for four; 8 experts, top-2, four tokens: 23.8 against 28.2).
-  if (T <= kW4TokenMax) {
+  // A route per wave reads and converts an expert's weights for every token that
+  // chose it, so this is for few tokens whose routes seldom share one.  FFNs of K
+  // = 4096, I = 2048, against the grouped products:
+  //   256 experts, top-6, e2m1: two tokens 40.0 us against 44.0, four 75 and 75
+  //   64 experts, top-6, four tokens: int4 76 against 79, e2m1 72 and 72
+  //   8 experts, top-4, four tokens: int4 35.6 against 36.6, e2m1 34.0 and 35.3
+  //   8 experts, top-6, four tokens: int4 48.8 against 40.7, e2m1 46.2 and 39.1
+  //   8 experts, top-8, three tokens: int4 43.0 against 39.4, e2m1 41.4 and 36.8
+  if (T <= kW4TokenMax && a.R <= 2 * (int64_t)a.E) {
     if (format == W4_MX) return launch_token<W4_MX, ELEM_BF16, 1>(a, weights, T, stream);
     return a.scale_elem == ELEM_F16 ? launch_token_int4<ELEM_F16>(a, weights, T, stream)
                                     : launch_token_int4<ELEM_BF16>(a, weights, T, stream);
