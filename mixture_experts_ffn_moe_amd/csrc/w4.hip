@@ -927,9 +927,16 @@ int grid_y(const W4Args& a, int tile) {
 template <int FMT, int XE, int SE, int GM, bool RAG, int NT, bool SWIGLU, int D>
 hipError_t launch_one(const W4Args& a, int tile, int token_lds, hipStream_t stream) {
   const int tiles = out_tiles<XE>(a), y = grid_y(a, tile);
-  // several tiles a workgroup once there are more workgroups than the GPU holds
+  // Several tiles a workgroup once there are some times more tiles than the 768 to
+  // 1,024 workgroups that the GPU holds at once.  FFNs of K = 4096, I = 2048, int4
+  // with zeros, by tiles of each product:
+  //   1,152 (16 tokens, 8 experts, top-2)   48 us with one, 53 with two, 79 with four
+  //   4,224 (16 tokens, 32 experts, top-4)  118, 112, 124
+  //   8,320 (32 tokens, 64 experts, top-4)  223, 203, 216
+  //   24,576 (32 tokens, 256 experts, top-6)  482, 413, 409
+  // and K = 2048, I = 1024: 12,288 (32 tokens, 256 experts, top-6) 156, 127, 123.
   const int64_t all = (int64_t)tiles * y;
-  const int run = all < 4096 ? 1 : all < 8192 ? 2 : 4;
+  const int run = all < 4096 ? 1 : all < 12288 ? 2 : 4;
   const int lds = token_lds + sum_lds<XE, NT>() + list_bytes(a);
   constexpr auto kernel = k_w4<FMT, XE, SE, GM, RAG, NT, SWIGLU, D>;
   if (lds > 65536) {
