@@ -656,7 +656,9 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const
  * routes per expert: its weights are read again for every 16 of them at most
  * (fewer where experts have few on average).  Sums are fp32 in a fixed order:
  * the same inputs give the same bits.  An infinite activation gives NaN or an
- * infinity.
+ * infinity.  MOE_W4_INT beside bf16 activations sums up to 31 times a scale
+ * group's activations: finite ones for which that leaves fp32 do so too.  A
+ * weight past fp32's largest (e8m0 253 and 254) is infinite.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_ALIGN,
  * MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 is a successful no-op.
  */

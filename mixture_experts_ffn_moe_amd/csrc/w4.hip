@@ -964,8 +964,11 @@ hipError_t launch_walk(const W4Args& a, hipStream_t stream) {
   // Tokens of one pass over the weights: 16, or 8 of more parts, so that two
   // steps of them fit the LDS.  Where the experts have few routes on average,
   // passes of fewer tokens leave room for more steps ahead, and an expert with
-  // more routes takes another pass (T = 32, 256 experts, top-6: 369 us with
-  // passes of 4, 392 with 8).
+  // more routes takes another pass.  At most a route an expert (T = 32, 256
+  // experts, top-6): 369 us with passes of 4, 392 with 8.  At most two (FFN of 16
+  // tokens in int4, 64 experts, top-6): K = 4096, I = 2048 197 us with half passes,
+  // 201 with whole ones; K = 2048, I = 1024 58 and 62; K = 1024, I = 768, whose
+  // tokens fit the LDS either way, 41 and 40.
   const int tokens = a.R / a.top_k;
   int tile = kTile / parts<FMT, XE>();
   if (a.ids && a.R <= a.E) tile = 4;
