@@ -51,14 +51,14 @@
 // need.  Where there are many tiles a workgroup takes several in a row,
 // requesting the next one's weights while it ends the last.
 //
-// Measured at K = 4096, I = 2048, 256 experts, top-6 (kernel times): 32 tokens
-// in e2m1 take 233 us for the first product (1.21 GB, 5.2 TB/s) and 128 us for
-// the second (4.8 TB/s); int4 with zero points 264 and 149 us, its conversion
-// keeping the vector units busy half of the time.  One token in int4 takes 15 us
-// (53 MB) and 9 us: the launch, finding the expert and bringing the token in are
-// half of that, the loads of all workgroups going out at once.  Streaming the
-// weights past the caches was slower (366 -> 381 us for the e2m1 FFN): a line of
-// 128 bytes is read in two steps.
+// Measured at K = 4096, I = 2048, 256 experts, top-6 (kernel times under the
+// profiler): 32 tokens in e2m1 take 241 us for the first product (1.21 GB, 5.0
+// TB/s) and 123 us for the second (4.9 TB/s); int4 with zero points 277 and 157
+// us, its conversion keeping the vector units busy half of the time.  One token in
+// int4 takes 14 us (53 MB) and 9 us: the launch, finding the expert and bringing
+// the token in are half of that, the loads of all workgroups going out at once.
+// Streaming the weights past the caches was slower (366 -> 381 us for the e2m1
+// FFN): a line of 128 bytes is read in two steps.
 #include <atomic>
 #include <type_traits>
 
