@@ -688,6 +688,125 @@ int fused_moe_w4(int32_t format, int32_t elem, const void* x, const void* w1, co
                  int32_t group, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * General router.
+ *
+ * moe_route_align routes by a softmax over the selected logits.  These calls
+ * cover the gates of other models, for moe_align and the forward to follow:
+ * with l the logits of a token,
+ *   s = softmax(l) over all experts (MOE_SCORE_SOFTMAX) or 1 / (1 + exp(-l))
+ *       (MOE_SCORE_SIGMOID);
+ *   c = s + bias, the scores that choose;
+ *   groups: the experts form n_group runs of E / n_group; a group's score is
+ *       the sum of its group_top (1 or 2) largest c, and only the topk_group
+ *       groups of the largest scores keep their experts;
+ *   topk_ids: the top_k largest c among those, in descending order;
+ *   topk_weights: scale * s of the chosen, with renormalize divided by the
+ *       chosen ones' sum first.
+ * Equal scores go to the lower index.  Scores are computed and compared in 64
+ * bits, so that the choice does not hang on an exponential's rounding in 32.
+ * An expert whose logit is -inf or NaN, or whose bias is, is masked: it is
+ * never chosen, and takes no part in a softmax where its logit is.  Where fewer
+ * than top_k experts are left, the rest of topk_ids is -1 (which the planner
+ * skips) and of topk_weights 0.  A logit of +inf counts as fp32's largest.
+ * Chosen scores whose sum is 0 in 64 bits get weights 0.
+ *   elem     MOE_ELEM_BF16, MOE_ELEM_F16 or MOE_ELEM_F32: logits (T, E).
+ *   bias     (E) fp32, or NULL for none.  It takes part in the choice only and
+ *            has no gradient.
+ * E <= 1024, top_k <= min(16, E), n_group <= 64 divides E, top_k <=
+ * topk_group * E / n_group, T <= 2^26 - 4.  Errors: MOE_ERR_NULL,
+ * MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_ALIGN, MOE_ERR_HIP.  T == 0 is
+ * a successful no-op.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scoring;
+
+int moe_route_topk(int32_t elem, const void* logits, const float* bias, int64_t T, int32_t E,
+                   int32_t top_k, int32_t scoring, int32_t n_group, int32_t topk_group,
+                   int32_t group_top, int32_t renormalize, float scale, int32_t* topk_ids,
+                   float* topk_weights, void* stream);
+
+/* Gradient of moe_route_topk's weights: d_logits (T, E) of the logits' type,
+ * every element written, from the same logits and options, topk_ids as the call
+ * wrote them and d_weights (T, top_k) fp32.  The choice itself has no gradient.
+ * An id outside [0, E) takes no part; an id that occurs twice gets both terms. */
+int moe_route_topk_backward(int32_t elem, const void* logits, const int32_t* topk_ids,
+                            const float* d_weights, int64_t T, int32_t E, int32_t top_k,
+                            int32_t scoring, int32_t renormalize, float scale, void* d_logits,
+                            void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * 8-bit linear layers: e4m3 values with a scale for each 128 of the
+ * contraction.
+ *
+ * fused_moe_fp8_blockwise runs whole expert FFNs forward.  These calls are its
+ * single steps, for dense layers around the experts, for experts with other
+ * activations, and for training: the quantizers, the product (dense, or over
+ * the rows of a plan), and the gradient of its weights.  The gradient of its
+ * input is the product again, of d_out quantized along its rows with the
+ * transposed weights.  A plan's rows are moe_permute's; e4m3 values and scales
+ * can themselves be permuted as MOE_ELEM_U8 / MOE_ELEM_F32 rows.
+ *
+ *   scale_type  MOE_SCALE_F32: fp32, amax / 448 (fused_moe_fp8_blockwise's
+ *               operands); MOE_SCALE_E8M0: uint8 powers of two 2^(c - 127), the
+ *               smallest at or above amax / 448 (255: NaN).  The matrix
+ *               instruction takes the latter itself, which is faster.
+ *   num_tokens_post_padded
+ *               rows in use (device); what lies behind them is neither read
+ *               nor written.  It counts as at most the buffers' rows.
+ * Sums: MOE_SCALE_F32 adds each 128's sum in fp32; inside 128 (and for
+ * MOE_SCALE_E8M0 throughout) the matrix instruction adds, whose sums keep about
+ * 16 bits of the products' norm (moe_mfma_probe), so outputs are bf16 or fp16.
+ * Every element of the output's rows in use is written.  The same inputs give
+ * the same bits.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_ALIGN, MOE_ERR_HIP.
+ */
+typedef enum { MOE_SCALE_F32 = 0, MOE_SCALE_E8M0 = 1 } moe_scale_type;
+
+/* x (M, K), elem MOE_ELEM_BF16, _F16 or _F32, K a multiple of 16:
+ *   q (M, K) e4m3, q_scale (M, ceil(K / 128)): a scale per 128 of a row;
+ *   qt (K, Mp) e4m3, q_t scale (K, Mp / 128), Mp = M rounded up to 128: x
+ *     transposed with a scale per 128 rows of a column, zeros for the rows from
+ *     M on (and from num_tokens_post_padded on, inside its last 128).
+ * Either q or qt may be NULL (with its scales).  amax is floored at 1e-30;
+ * values are x * (1 / scale) rounded to nearest even.  A group with an infinity
+ * or a NaN comes out as NaN.  num_tokens_post_padded may be NULL: M rows. */
+int moe_fp8_quant(int32_t elem, int32_t scale_type, const void* x, int64_t M, int64_t K,
+                  const int32_t* num_tokens_post_padded, void* q, void* q_scale, void* qt,
+                  void* qt_scale, void* stream);
+
+/* Weights w (E, N, K), a scale per 128 x 128 block: q (E, N, K), q_scale (E,
+ * ceil(N / 128), ceil(K / 128)); unless qt is NULL also transposed, qt (E, K, N)
+ * and qt_scale (E, ceil(K / 128), ceil(N / 128)).  K is a multiple of 16, and with
+ * qt N too. */
+int moe_fp8_quant_weights(int32_t elem, int32_t scale_type, const void* w, int64_t E, int64_t N,
+                          int64_t K, void* q, void* q_scale, void* qt, void* qt_scale, void* stream);
+
+/* out[m] = W[e] . x[m], out (M, N) of elem (MOE_ELEM_BF16 or MOE_ELEM_F16): x (M,
+ * K) and w (E, N, K) e4m3, x_scale (M, ceil(K / 128)), w_scale (E, ceil(N / 128),
+ * ceil(K / 128)); K a multiple of 16.
+ * expert_ids NULL: one layer (E = 1).  Else the planner's expert_ids for blocks of
+ * block_m rows (ceil(M / block_m) of them), and the rows are the plan's, below
+ * num_tokens_post_padded; a block whose id is outside [0, E) gives zeros. */
+int moe_fp8_linear(int32_t elem, int32_t scale_type, const void* x, const void* x_scale,
+                   const void* w, const void* w_scale, const int32_t* expert_ids,
+                   const int32_t* num_tokens_post_padded, void* out, int64_t M, int64_t K, int64_t N,
+                   int32_t E, int32_t block_m, void* stream);
+
+/* Gradient of moe_fp8_linear's weights: dw (E, N, K)[e] = sum of d_out[m]^T x[m]
+ * over the expert's rows, of elem (MOE_ELEM_BF16 or MOE_ELEM_F16), from both
+ * quantized along the rows: dyt (N, M) and xt (K, M) e4m3, M a multiple of 128
+ * (moe_fp8_quant's qt), scales (N, M / 128) and (K, M / 128).
+ * expert_ids NULL: one layer (E = 1), all M rows.  Else the plan's n_blocks ids
+ * for blocks of block_m = 128 or 256 rows, an expert's in one run, as the planner
+ * lays them out; an expert without rows gets zeros.  Padding rows must be zeros
+ * (moe_permute writes them so).  M == 0 writes zeros. */
+int moe_fp8_linear_dw(int32_t elem, int32_t scale_type, const void* dyt, const void* dyt_scale,
+                      const void* xt, const void* xt_scale, const int32_t* expert_ids,
+                      const int32_t* num_tokens_post_padded, void* dw, int64_t M, int64_t N, int64_t K,
+                      int32_t E, int32_t block_m, int64_t n_blocks, void* stream);
+
+/*
  * Diagnostic, not a step of the forward: one 128-wide K step of the matrix
  * instruction each dtype's kernels use, D = C + A . B^T, per 16 x 16 tile,
  * through the kernels' own operand layout and instruction wrappers.  The

@@ -19,6 +19,10 @@ Entry points (same names as the C ABI):
       tokens into the rows of a plan and back, with the gradients
   moe_w4_matvec, fused_moe_w4
       products with 4-bit weights for a few tokens, alone and as the experts' FFN
+  moe_route_topk, moe_route_topk_backward
+      router with softmax or sigmoid scores, a balancing bias and expert groups
+  moe_fp8_quant, moe_fp8_quant_weights, moe_fp8_linear, moe_fp8_linear_dw
+      8-bit linear layers with a scale per 128, dense or over a plan's rows, with gradients
 plus the host helpers moe_align_capacity, moe_workspace_size,
 moe_workspace_layout, moe_ring_layout, moe_select_split and moe_select_block_m.
 ``split=2`` runs the persistent ring mode (block_m 16 or 32).
@@ -42,6 +46,8 @@ __all__ = [
     "moe_route_rows", "moe_permute", "moe_permute_backward", "moe_unpermute",
     "moe_unpermute_backward", "moe_route_backward",
     "moe_w4_matvec", "moe_w4_workspace_size", "fused_moe_w4",
+    "moe_route_topk", "moe_route_topk_backward",
+    "moe_fp8_quant", "moe_fp8_quant_weights", "moe_fp8_linear", "moe_fp8_linear_dw",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi355x.so")
@@ -61,6 +67,8 @@ EXPORTED_SYMBOLS = (
     "moe_route_rows", "moe_permute", "moe_permute_backward", "moe_unpermute",
     "moe_unpermute_backward", "moe_route_backward",
     "moe_w4_matvec", "moe_w4_workspace_size", "fused_moe_w4",
+    "moe_route_topk", "moe_route_topk_backward",
+    "moe_fp8_quant", "moe_fp8_quant_weights", "moe_fp8_linear", "moe_fp8_linear_dw",
 )
 
 _STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SHAPE", -3: "MOE_ERR_UNSUPPORTED",
@@ -137,6 +145,13 @@ def lib():
     L.moe_w4_workspace_size.argtypes = [_I64, _I64, _I64, _I32, ctypes.POINTER(_SZ)]
     L.fused_moe_w4.argtypes = [_I32, _I32] + [_P] * 10 + [_I64, _I64, _I64, _I32, _I32, _I32, _P,
                                                           _SZ, _P]
+    L.moe_route_topk.argtypes = [_I32, _P, _P, _I64] + [_I32] * 7 + [ctypes.c_float, _P, _P, _P]
+    L.moe_route_topk_backward.argtypes = [_I32, _P, _P, _P, _I64] + [_I32] * 4 + [ctypes.c_float, _P,
+                                                                                  _P]
+    L.moe_fp8_quant.argtypes = [_I32, _I32, _P, _I64, _I64, _P, _P, _P, _P, _P, _P]
+    L.moe_fp8_quant_weights.argtypes = [_I32, _I32, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P]
+    L.moe_fp8_linear.argtypes = [_I32, _I32] + [_P] * 7 + [_I64, _I64, _I64, _I32, _I32, _P]
+    L.moe_fp8_linear_dw.argtypes = [_I32, _I32] + [_P] * 7 + [_I64, _I64, _I64, _I32, _I32, _I64, _P]
     for name in EXPORTED_SYMBOLS:
         if name != "moe_last_error":
             getattr(L, name).restype = ctypes.c_int
@@ -823,6 +838,244 @@ def fused_moe_w4(fmt, x, w1, w1_scale, w1_zero, w2, w2_scale, w2_zero, topk_ids,
     _enqueue(lib().fused_moe_w4, dev, stream, f, elem, xp, *p1, *p2, ids, wt, out.data_ptr(), T, K,
              N, E, k, group, workspace.data_ptr(),
              workspace.numel() * workspace.element_size())
+    return out
+
+
+def _float_elem(t, name):
+    elem = _elem(t, name)
+    if elem > 2:
+        raise MoeError(-3, f"{name} must be bf16, fp16 or fp32 (got {t.dtype})")
+    return elem
+
+
+# Scorings of the general router (moe_scoring of the C ABI).
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def _route_options(logits, scoring):
+    """Sizes, element type and scoring code of a router call."""
+    T, E = _matrix(logits, "logits")
+    code = _SCORING.get(scoring)
+    if code is None:
+        raise MoeError(-3, f"unknown scoring {scoring!r}: 'softmax' or 'sigmoid'")
+    return T, E, _float_elem(logits, "logits"), code
+
+
+def moe_route_topk(logits, top_k, bias=None, scoring="softmax", n_group=1, topk_group=1, group_top=1,
+                   renormalize=True, scale=1.0, stream=None, out=None):
+    """General router: (T, E) bf16, fp16 or fp32 logits -> (topk_ids (T, top_k)
+    int32, topk_weights (T, top_k) fp32).
+
+    Scores are the softmax over all experts or the sigmoid of each logit; the
+    ``top_k`` largest of score + ``bias`` ((E) fp32 or None) are chosen, equal
+    ones to the lower index, among the experts of the ``topk_group`` of
+    ``n_group`` groups whose ``group_top`` (1 or 2) largest add up to most.
+    Weights are the chosen ones' scores without the bias, divided by their sum
+    with ``renormalize``, times ``scale``.  A logit of -inf or NaN masks an
+    expert; where fewer than top_k are left, ids are -1 and weights 0.  The
+    planner (moe_align) takes the ids as they are.  ``out`` may pass the two
+    preallocated.  moe_route_topk_backward is its gradient: with gradients
+    enabled the call refuses logits that require one (make it inside a
+    torch.autograd.Function)."""
+    T, E, elem, code = _route_options(logits, scoring)
+    dev = logits.device
+    lp = _operand(logits, "logits", logits.dtype, (T, E), dev)
+    bp = None if bias is None else _operand(bias, "bias", torch.float32, (E,), dev)
+    ids, w = (None, None) if out is None else out
+    ids = _output(ids, "topk_ids", (T, top_k), torch.int32, dev, stream)
+    w = _output(w, "topk_weights", (T, top_k), torch.float32, dev, stream)
+    _outside_autograd(logits)
+    _enqueue(lib().moe_route_topk, dev, stream, elem, lp, bp, T, E, top_k, code, n_group, topk_group,
+             group_top, int(renormalize), scale, ids.data_ptr(), w.data_ptr())
+    return ids, w
+
+
+def moe_route_topk_backward(logits, topk_ids, d_weights, scoring="softmax", renormalize=True,
+                            scale=1.0, stream=None, out=None):
+    """Gradient of moe_route_topk's weights with respect to its logits, (T, E)
+    of their type, from the same logits and options, topk_ids as it returned
+    them and the weights' gradient (T, top_k) fp32."""
+    T, E, elem, code = _route_options(logits, scoring)
+    dev = logits.device
+    _, k = _matrix(topk_ids, "topk_ids")
+    lp = _operand(logits, "logits", logits.dtype, (T, E), dev)
+    ids = _operand(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    dw = _operand(d_weights, "d_weights", torch.float32, (T, k), dev)
+    out = _output(out, "out", (T, E), logits.dtype, dev, stream)
+    _outside_autograd(logits, d_weights)
+    _enqueue(lib().moe_route_topk_backward, dev, stream, elem, lp, ids, dw, T, E, k, code,
+             int(renormalize), scale, out.data_ptr())
+    return out
+
+
+# Scale types of 8-bit values (moe_scale_type of the C ABI).
+_SCALE = {"f32": (0, torch.float32), "e8m0": (1, torch.uint8)}
+
+
+def _scale_kind(name):
+    kind = _SCALE.get(name)
+    if kind is None:
+        raise MoeError(-3, f"unknown scale type {name!r}: 'f32' or 'e8m0'")
+    return kind
+
+
+def _groups(n):
+    return -(-n // 128)
+
+
+def moe_fp8_quant(x, scale_type="f32", rows=True, columns=False, num_tokens_post_padded=None,
+                  stream=None, out=None):
+    """x (M, K) bf16, fp16 or fp32, K a multiple of 16, into e4m3:
+    (q, q_scale, qt, qt_scale), None for the forms not asked for.
+
+    ``rows``: q (M, K) with a scale per 128 of a row, q_scale (M, ceil(K/128)).
+    ``columns``: x transposed with a scale per 128 rows of a column, qt (K, Mp)
+    and qt_scale (K, Mp/128), Mp = M rounded up to 128 with zeros behind M; what
+    moe_fp8_linear_dw takes.  Scales are fp32 amax / 448 ("f32") or uint8 powers
+    of two at or above that ("e8m0").  With ``num_tokens_post_padded`` (a plan's
+    device count) rows behind it, and groups of 128 that begin behind it, are
+    left as they are (unspecified in new tensors).  ``out`` may pass the four
+    preallocated."""
+    M, K = _matrix(x, "x")
+    dev = x.device
+    elem = _float_elem(x, "x")
+    code, kind = _scale_kind(scale_type)
+    xp = _operand(x, "x", x.dtype, (M, K), dev)
+    ntp = None if num_tokens_post_padded is None else _operand(
+        num_tokens_post_padded, "num_tokens_post_padded", torch.int32, (1,), dev)
+    if not rows and not columns:
+        raise MoeError(-2, "rows or columns (or both) must be asked for")
+    q, qs, qt, qts = (None,) * 4 if out is None else out
+    f8, G = torch.float8_e4m3fn, _groups(M)
+    q = _output(q, "q", (M, K), f8, dev, stream) if rows else None
+    qs = _output(qs, "q_scale", (M, _groups(K)), kind, dev, stream) if rows else None
+    qt = _output(qt, "qt", (K, 128 * G), f8, dev, stream) if columns else None
+    qts = _output(qts, "qt_scale", (K, G), kind, dev, stream) if columns else None
+    _outside_autograd(x)
+    _enqueue(lib().moe_fp8_quant, dev, stream, elem, code, xp, M, K, ntp, _ptr(q), _ptr(qs), _ptr(qt),
+             _ptr(qts))
+    return q, qs, qt, qts
+
+
+def moe_fp8_quant_weights(w, scale_type="f32", transposed=False, stream=None, out=None):
+    """Weights w (E, N, K) bf16, fp16 or fp32 into e4m3 with a scale per 128 x
+    128 block: (q (E, N, K), q_scale (E, ceil(N/128), ceil(K/128)), qt, qt_scale).
+    ``transposed``: qt (E, K, N) and qt_scale, the weights with which moe_fp8_linear
+    computes the gradient of its input; else None.  K, and N if transposed, are
+    multiples of 16.  Scales as moe_fp8_quant's."""
+    if len(w.shape) != 3:
+        raise MoeError(-2, f"w must have shape (E, N, K) (got {tuple(w.shape)})")
+    E, N, K = w.shape
+    dev = w.device
+    elem = _float_elem(w, "w")
+    code, kind = _scale_kind(scale_type)
+    wp = _operand(w, "w", w.dtype, (E, N, K), dev)
+    q, qs, qt, qts = (None,) * 4 if out is None else out
+    f8, NB, KB = torch.float8_e4m3fn, _groups(N), _groups(K)
+    q = _output(q, "q", (E, N, K), f8, dev, stream)
+    qs = _output(qs, "q_scale", (E, NB, KB), kind, dev, stream)
+    qt = _output(qt, "qt", (E, K, N), f8, dev, stream) if transposed else None
+    qts = _output(qts, "qt_scale", (E, KB, NB), kind, dev, stream) if transposed else None
+    _outside_autograd(w)
+    _enqueue(lib().moe_fp8_quant_weights, dev, stream, elem, code, wp, E, N, K, _ptr(q), _ptr(qs),
+             _ptr(qt), _ptr(qts))
+    return q, qs, qt, qts
+
+
+def _out_elem(out, dtype):
+    """Element type of an 8-bit product's output."""
+    dtype = dtype if out is None else out.dtype
+    elem = _ELEM.get(dtype)
+    if elem is None or elem > 1:
+        raise MoeError(-3, f"the output must be bf16 or fp16 (got {dtype})")
+    return elem, dtype
+
+
+def _scale_of(t, name):
+    code = {torch.float32: 0, torch.uint8: 1}.get(t.dtype)
+    if code is None:
+        raise MoeError(-3, f"{name} must be fp32 or uint8 e8m0 (got {t.dtype})")
+    return code
+
+
+def moe_fp8_linear(x, x_scale, w, w_scale, expert_ids=None, num_tokens_post_padded=None, block_m=0,
+                   dtype=torch.bfloat16, stream=None, out=None):
+    """Products of e4m3 rows x (M, K) with e4m3 weights w (E, N, K): (M, N) of
+    ``dtype`` (bf16 or fp16; ``out``'s, if given).  x_scale (M, ceil(K/128)) and w_scale (E,
+    ceil(N/128), ceil(K/128)) are both fp32 or both uint8 e8m0; K is a multiple
+    of 16.
+
+    Without ``expert_ids`` one layer, E = 1.  With a plan's expert_ids,
+    num_tokens_post_padded and block_m the rows are the plan's (moe_permute's):
+    each block of block_m rows takes its expert's weights; rows from
+    num_tokens_post_padded on are left as they are (unspecified in a new
+    tensor).  The gradient of x is this call on d_out quantized along its rows
+    and the transposed weights (moe_fp8_quant_weights), the weights' is
+    moe_fp8_linear_dw."""
+    M, K = _matrix(x, "x")
+    dev = x.device
+    if len(w.shape) != 3:
+        raise MoeError(-2, f"w must have shape (E, N, K) (got {tuple(w.shape)})")
+    E, N, _ = w.shape
+    _on_gpu(x, "x")
+    kind = _scale_of(x_scale, "x_scale")
+    f8 = torch.float8_e4m3fn
+    xp = _operand(x, "x", f8, (M, K), dev)
+    xs = _operand(x_scale, "x_scale", x_scale.dtype, (M, _groups(K)), dev)
+    wp = _operand(w, "w", f8, (E, N, K), dev)
+    ws = _operand(w_scale, "w_scale", x_scale.dtype, (E, _groups(N), _groups(K)), dev)
+    ids, ntp = _plan_blocks(expert_ids, num_tokens_post_padded, block_m, M, dev)
+    elem, dtype = _out_elem(out, dtype)
+    out = _output(out, "out", (M, N), dtype, dev, stream)
+    _enqueue(lib().moe_fp8_linear, dev, stream, elem, kind, xp, xs, wp, ws, ids, ntp, out.data_ptr(), M, K,
+             N, E, block_m)
+    return out
+
+
+def _plan_blocks(expert_ids, ntp, block_m, rows, dev):
+    """Checks a plan's blocks (None: no plan); at least those of ``rows`` rows, if given."""
+    if expert_ids is None:
+        if ntp is not None or block_m:
+            raise MoeError(-2, "num_tokens_post_padded and block_m belong to expert_ids, which is missing")
+        return None, None
+    if ntp is None:
+        raise MoeError(-1, "expert_ids need num_tokens_post_padded")
+    n = expert_ids.numel()
+    ids = _operand(expert_ids, "expert_ids", torch.int32, (n,), dev)
+    if block_m < 1 or (rows is not None and n < -(-rows // block_m)):
+        raise MoeError(-2, f"{n} expert_ids for {rows} rows in blocks of {block_m}")
+    return ids, _operand(ntp, "num_tokens_post_padded", torch.int32, (1,), dev)
+
+
+def moe_fp8_linear_dw(dyt, dyt_scale, xt, xt_scale, num_experts=1, expert_ids=None,
+                      num_tokens_post_padded=None, block_m=0, dtype=torch.bfloat16, stream=None,
+                      out=None):
+    """Gradient of moe_fp8_linear's weights, (num_experts, N, K) of ``dtype``
+    (bf16 or fp16; ``out``'s, if given): for each expert the sum of d_out[m]^T x[m] over its rows.
+
+    dyt (N, M) and xt (K, M) e4m3 are d_out and x as moe_fp8_quant's columns
+    give them (M a multiple of 128), with scales (N, M/128) and (K, M/128), both
+    fp32 or both uint8 e8m0.  Without ``expert_ids`` one layer; with a plan's
+    (blocks of 128 or 256 rows, padding rows zeros) each expert's own rows, zeros
+    for an expert without any."""
+    N, M = _matrix(dyt, "dyt")
+    K, _ = _matrix(xt, "xt")
+    dev = dyt.device
+    _on_gpu(dyt, "dyt")
+    _experts(num_experts)
+    kind = _scale_of(dyt_scale, "dyt_scale")
+    f8 = torch.float8_e4m3fn
+    if M % 128:
+        raise MoeError(-2, f"dyt must have whole groups of 128 columns (got {M})")
+    dp = _operand(dyt, "dyt", f8, (N, M), dev)
+    ds = _operand(dyt_scale, "dyt_scale", dyt_scale.dtype, (N, M // 128), dev)
+    xp = _operand(xt, "xt", f8, (K, M), dev)
+    xs = _operand(xt_scale, "xt_scale", dyt_scale.dtype, (K, M // 128), dev)
+    ids, ntp = _plan_blocks(expert_ids, num_tokens_post_padded, block_m, None, dev)
+    elem, dtype = _out_elem(out, dtype)
+    out = _output(out, "out", (num_experts, N, K), dtype, dev, stream)
+    _enqueue(lib().moe_fp8_linear_dw, dev, stream, elem, kind, dp, ds, xp, xs, ids, ntp, out.data_ptr(), M,
+             N, K, num_experts, block_m, 0 if ids is None else expert_ids.numel())
     return out
 
 

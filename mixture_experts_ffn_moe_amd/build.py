@@ -18,8 +18,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
-SOURCES = ["abi.hip", "abi_rows.hip", "abi_w4.hip", "align.hip", "moe_kernels.hip",
-           "moe_tiled.hip", "probe.hip", "rows.hip", "w4.hip"]
+SOURCES = ["abi.hip", "abi_fp8.hip", "abi_route.hip", "abi_rows.hip", "abi_w4.hip", "align.hip",
+           "fp8_linear.hip", "moe_kernels.hip", "moe_tiled.hip", "probe.hip", "quant.hip",
+           "route.hip", "rows.hip", "w4.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,6 +1,7 @@
-// ops.h -- internal launchers of the operators around the plan (rows.hip) and
-// of the 4-bit products (w4.hip), and the error reporting they share with
-// abi.hip.
+// ops.h -- internal launchers of the operators around the plan (rows.hip), of
+// the 4-bit products (w4.hip), the general router (route.hip), the 8-bit
+// quantizers (quant.hip) and the 8-bit linear layers (fp8_linear.hip), and the
+// error reporting they share with abi.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -70,3 +71,63 @@ hipError_t launch_w4(int format, const W4Args& a, hipStream_t stream);
 constexpr int kW4TokenMax = 4;
 hipError_t launch_w4_down(int format, const W4Args& a, const float* weights, float* y, int T,
                           hipStream_t stream);
+
+// The general router.  Scores in the order of moe_scoring.
+enum : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1 };
+constexpr int kRouteMaxExperts = 1024, kRouteMaxTopK = 16, kRouteMaxGroups = 64;
+
+struct RouteArgs {
+  const void* logits;  // (T, E) elem
+  const float* bias;   // (E), or null
+  int64_t T;
+  int E, top_k, elem, scoring;
+  int n_group, topk_group, group_top;
+  int renormalize;
+  float scale;
+};
+
+hipError_t launch_route_topk(const RouteArgs& a, int32_t* ids, float* weights, hipStream_t stream);
+hipError_t launch_route_topk_backward(const RouteArgs& a, const int32_t* ids, const float* d_weights,
+                                      void* d_logits, hipStream_t stream);
+
+// Scales of 8-bit values, in the order of moe_scale_type.
+enum : int { SCALE_F32 = 0, SCALE_E8M0 = 1 };
+constexpr int scale_bytes(int type) { return type == SCALE_F32 ? 4 : 1; }
+
+// e4m3 values of x (M, K) with a scale per 128 of a row (q) and, transposed, per
+// 128 of a column (qt); either may be null.
+struct QuantArgs {
+  const void* x;
+  const int32_t* ntp;  // rows in use (device scalar), or null for all
+  uint8_t* q;          // (M, K)
+  void* qs;            // (M, ceil(K / 128))
+  uint8_t* qt;         // (K, Mp), Mp = M rounded up to 128
+  void* qts;           // (K, Mp / 128)
+  int64_t M, K;
+  int elem, scale_type;
+};
+hipError_t launch_quant(const QuantArgs& a, hipStream_t stream);
+// The same for weights (E, N, K) with a scale per 128 x 128 block: q (E, N, K), qs
+// (E, NB, KB), and transposed (qt not null) qt (E, K, N), qts (E, KB, NB).
+hipError_t launch_quant_weights(const void* w, int64_t E, int64_t N, int64_t K, int elem,
+                                int scale_type, uint8_t* q, void* qs, uint8_t* qt, void* qts,
+                                hipStream_t stream);
+
+// out[m, n] = sum_k X[m, k] W[n, k] on e4m3 values with scales per 128 of k.
+//   layer (dw = 0): X are rows, W the weights of one expert (a scale per 128 x
+//     128 block); with a plan, block b of block_m rows takes expert experts[b].
+//   gradient (dw = 1): X is dy transposed, W is x transposed (scales per row of
+//     both), k the rows; with a plan, expert e sums over the rows of its blocks.
+struct Fp8Args {
+  const uint8_t* x;  // (M, K)
+  const void* xs;    // (M, ceil(K / 128))
+  const uint8_t* w;  // (E, N, K); dw: (N, K)
+  const void* ws;    // (E, ceil(N / 128), ceil(K / 128)); dw: (N, K / 128)
+  const int32_t* experts;  // expert of each block, or null (one layer)
+  const int32_t* ntp;      // rows in use (device scalar)
+  void* out;               // (M, N); dw: (E, M, N)
+  int64_t M, N, K;
+  int E, block_m, n_blocks;
+  int oelem, scale_type, dw;
+};
+hipError_t launch_fp8_linear(const Fp8Args& a, hipStream_t stream);

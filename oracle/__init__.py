@@ -19,6 +19,8 @@ router   the gate's routing from router logits: softmax over the experts,
 w4       products with 4-bit weights, and the FFN of a few tokens.
 rows     tokens into the rows of a plan and back, their gradients and the
          router's.
+route_topk  the general router: scores, bias, groups, top-k, and its gradient.
+fp8      quantizers with a scale per 128, and products of such values.
 
 Every function cites the page and passage of the source pages it follows.
 The sources are five web pages on fused MoE kernels:

@@ -1,0 +1,122 @@
+"""Refusals of the 8-bit quantizers and linear layers (CPU only)."""
+
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_ffn_moe_amd as moe
+
+from .test_rows_abi_cpu import Fake as Face
+
+P = ctypes.c_void_p
+F, ODD = P(1 << 20), P((1 << 20) + 8)
+NULL, SHAPE, UNSUPPORTED, ALIGN = -1, -2, -3, -4
+
+
+class Fake(Face):
+    requires_grad = False
+
+
+def quant(elem=0, kind=0, x=F, M=4, K=64, ntp=None, q=F, qs=F, qt=F, qts=F):
+    return moe.lib().moe_fp8_quant(elem, kind, x, M, K, ntp, q, qs, qt, qts, None)
+
+
+def weights(elem=0, kind=0, w=F, E=2, N=32, K=64, q=F, qs=F, qt=F, qts=F):
+    return moe.lib().moe_fp8_quant_weights(elem, kind, w, E, N, K, q, qs, qt, qts, None)
+
+
+def linear(elem=0, kind=0, x=F, xs=F, w=F, ws=F, ids=None, ntp=None, out=F, M=4, K=64, N=32, E=1, bm=0):
+    return moe.lib().moe_fp8_linear(elem, kind, x, xs, w, ws, ids, ntp, out, M, K, N, E, bm, None)
+
+
+def dw(elem=0, kind=0, dy=F, dys=F, x=F, xs=F, ids=None, ntp=None, out=F, M=128, N=32, K=64, E=1, bm=0, nb=0):
+    return moe.lib().moe_fp8_linear_dw(elem, kind, dy, dys, x, xs, ids, ntp, out, M, N, K, E, bm, nb, None)
+
+
+PLAN = dict(ids=F, ntp=F, E=3, bm=128)
+
+
+@pytest.mark.parametrize("call", [quant, weights, linear, dw])
+@pytest.mark.parametrize("bad", [dict(elem=-1), dict(elem=3), dict(kind=2), dict(kind=-1)])
+def test_types(call, bad):
+    assert call(**bad) == UNSUPPORTED
+    assert moe.lib().moe_last_error()
+
+
+def test_outputs_are_16_bits():
+    assert linear(elem=2) == UNSUPPORTED and dw(elem=2) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("call,bad,status", [
+    (quant, dict(M=-1), SHAPE), (quant, dict(K=0), SHAPE), (quant, dict(K=24), SHAPE), (quant, dict(K=1 << 31), UNSUPPORTED),
+    (quant, dict(M=1 << 31), UNSUPPORTED), (quant, dict(M=1 << 24), UNSUPPORTED),
+    (quant, dict(M=1 << 27, K=1 << 20, qt=None, qts=None), UNSUPPORTED), (quant, dict(q=None, qt=None), NULL),
+    (weights, dict(E=-1), SHAPE), (weights, dict(N=0), SHAPE), (weights, dict(N=24), SHAPE), (weights, dict(K=8), SHAPE),
+    (weights, dict(E=1 << 16), UNSUPPORTED), (weights, dict(N=1 << 24), UNSUPPORTED),
+    (linear, dict(M=-1), SHAPE), (linear, dict(K=8), SHAPE), (linear, dict(N=0), SHAPE), (linear, dict(E=0), SHAPE),
+    (linear, dict(E=2), SHAPE), (linear, dict(N=1 << 21), UNSUPPORTED), (linear, dict(M=1 << 26, N=1 << 19), UNSUPPORTED),
+    (linear, {**PLAN, "bm": 48}, UNSUPPORTED), (linear, {**PLAN, "bm": 0}, UNSUPPORTED), (linear, {**PLAN, "ntp": None}, NULL),
+    (linear, {**PLAN, "ntp": P((1 << 20) + 2)}, ALIGN),
+    (dw, dict(M=-128), SHAPE), (dw, dict(M=64), SHAPE), (dw, dict(N=0), SHAPE), (dw, dict(K=0), SHAPE), (dw, dict(E=0), SHAPE),
+    (dw, dict(E=2), SHAPE), (dw, {**PLAN, "bm": 64}, UNSUPPORTED), (dw, {**PLAN, "nb": -1}, SHAPE),
+    (dw, {**PLAN, "ntp": None}, NULL), (dw, dict(N=1 << 26, K=1 << 19), UNSUPPORTED)])
+def test_sizes(call, bad, status):
+    assert call(**bad) == status
+
+
+@pytest.mark.parametrize("call,names", [
+    (quant, ("x", "qs", "qts")), (weights, ("w", "q", "qs", "qts")), (linear, ("x", "xs", "w", "ws", "out")),
+    (dw, ("dy", "dys", "x", "xs", "out"))])
+def test_pointers(call, names):
+    for n in names:
+        assert call(**{n: None}) == NULL, n
+        assert call(**{n: ODD}) == ALIGN, n
+
+
+def test_empty_calls_launch_nothing():
+    assert quant(M=0, x=None, q=None, qs=None, qt=None, qts=None) == 0
+    assert weights(E=0, w=None, q=None, qs=None, qt=None, qts=None) == 0
+    assert linear(M=0, x=None, xs=None, w=None, ws=None, out=None) == 0
+
+
+def test_binding():
+    f8, f32, u8, i32 = torch.float8_e4m3fn, torch.float32, torch.uint8, torch.int32
+    x, xs, w, ws = Fake((4, 64), f8), Fake((4, 1), f32), Fake((1, 32, 64), f8), Fake((1, 1, 1), f32)
+    out, ids, ntp = Fake((4, 32)), Fake((1,), i32), Fake((1,), i32)
+    dy, dys, xt, xts, g = Fake((32, 128), f8), Fake((32, 1), f32), Fake((64, 128), f8), Fake((64, 1), f32), Fake((1, 32, 64))
+    grad = Fake((4, 64))
+    grad.requires_grad = True
+    bad = [
+        (lambda: moe.moe_fp8_quant(Fake((4, 64), u8)), UNSUPPORTED),
+        (lambda: moe.moe_fp8_quant(Fake((4, 64)), "e5m2"), UNSUPPORTED),
+        (lambda: moe.moe_fp8_quant(Fake((4, 64)), rows=False), SHAPE),
+        (lambda: moe.moe_fp8_quant(Fake((64,))), SHAPE),
+        (lambda: moe.moe_fp8_quant(Fake((4, 64), dense=False)), SHAPE),
+        (lambda: moe.moe_fp8_quant(grad, out=(Fake((4, 64), f8), xs, None, None)), UNSUPPORTED),
+        (lambda: moe.moe_fp8_quant(Fake((4, 64)), out=(Fake((4, 63), f8), xs, None, None)), SHAPE),
+        (lambda: moe.moe_fp8_quant(Fake((4, 64)), "e8m0", out=(x, xs, None, None)), UNSUPPORTED),
+        (lambda: moe.moe_fp8_quant_weights(Fake((32, 64))), SHAPE),
+        (lambda: moe.moe_fp8_linear(Fake((4, 64), u8), xs, w, ws, out=out), UNSUPPORTED),
+        (lambda: moe.moe_fp8_linear(x, Fake((4, 2), f32), w, ws, out=out), SHAPE),
+        (lambda: moe.moe_fp8_linear(x, Fake((4, 1)), w, ws, out=out), UNSUPPORTED),
+        (lambda: moe.moe_fp8_linear(x, Fake((4, 1), u8), w, ws, out=out), UNSUPPORTED),
+        (lambda: moe.moe_fp8_linear(x, xs, Fake((32, 64), f8), ws, out=out), SHAPE),
+        (lambda: moe.moe_fp8_linear(x, xs, Fake((1, 32, 80), f8), ws, out=out), SHAPE),
+        (lambda: moe.moe_fp8_linear(x, xs, w, ws, out=Fake((4, 32), f32)), UNSUPPORTED),
+        (lambda: moe.moe_fp8_linear(x, xs, w, ws, dtype=f32), UNSUPPORTED),
+        (lambda: moe.moe_fp8_linear(x, xs, w, ws, out=Fake((4, 31))), SHAPE),
+        (lambda: moe.moe_fp8_linear(x, xs, w, ws, ids, None, 16, out=out), NULL),
+        (lambda: moe.moe_fp8_linear(x, xs, w, ws, None, ntp, 16, out=out), SHAPE),
+        (lambda: moe.moe_fp8_linear(x, xs, w, ws, Fake((0,), i32), ntp, 16, out=out), SHAPE),
+        (lambda: moe.moe_fp8_linear(x, xs, w, ws, Fake((1,), f32), ntp, 16, out=out), UNSUPPORTED),
+        (lambda: moe.moe_fp8_linear_dw(Fake((32, 64), f8), dys, xt, xts, out=g), SHAPE),
+        (lambda: moe.moe_fp8_linear_dw(dy, dys, Fake((64, 256), f8), xts, out=g), SHAPE),
+        (lambda: moe.moe_fp8_linear_dw(dy, dys, xt, Fake((64, 1), u8), out=g), UNSUPPORTED),
+        (lambda: moe.moe_fp8_linear_dw(dy, dys, xt, xts, 0, out=g), SHAPE),
+        (lambda: moe.moe_fp8_linear_dw(dy, dys, xt, xts, 2, out=g), SHAPE),
+    ]
+    for i, (call, status) in enumerate(bad):
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.status == status, (i, e.value)

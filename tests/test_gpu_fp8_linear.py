@@ -1,0 +1,217 @@
+"""GPU parity of the 8-bit linear layers and of their weights' gradient against
+fp64 products of what the codes and scales stand for (oracle/fp8.py).
+
+Two gates.  Exact: whole values of at most 2, scales that are powers of two near
+one; every sum is a whole multiple of a power of two below 2^16, so the result is
+the exact one, rounded once.  Random: each element within 6 standard deviations of
+the oracle's error model plus half a step of the output's type, and the whole
+within that half step in the 2-norm."""
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_ffn_moe_amd as moe
+from oracle import fp8
+from oracle.codecs import e4m3_encode
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TINY = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25}
+KINDS = ("f32", "e8m0")
+MARK = 1234.0
+
+
+def up(n, to=128):
+    return -(-n // to)
+
+
+def operand(shape, scales, kind, rng, exact):
+    """(codes, scales) as numpy."""
+    if exact:
+        q = e4m3_encode(rng.integers(-2, 3, shape).astype(float))
+        e = rng.integers(-1, 2, scales)
+    else:
+        q = e4m3_encode(np.clip(rng.normal(size=shape) * 100, -448, 448))
+        e = rng.integers(-9, -6, scales)
+    if kind == "e8m0":
+        return q, (e + 127).astype(np.uint8)
+    return q, (2.0 ** e * (1 if exact else rng.uniform(1, 2, scales))).astype(np.float32)
+
+
+def gpu(pair):
+    q, s = pair
+    return torch.from_numpy(q).cuda().view(torch.float8_e4m3fn), torch.from_numpy(s).cuda()
+
+
+def close(out, x, w, elem, exact):
+    """out against x @ w.T (fp64 values)."""
+    y, sigma = fp8.product(x, w)
+    got = out.double().cpu().numpy()
+    if exact:
+        want = torch.from_numpy(y).to(TYPES[elem]).double().numpy()
+        assert np.array_equal(got, want), np.argwhere(got != want)[:5]
+        return
+    tol = HALF[elem] * np.abs(y) + TINY[elem] + 6 * sigma * (1 + HALF[elem])
+    assert (np.abs(got - y) <= tol).all(), float((np.abs(got - y) / tol).max())
+    norm = np.linalg.norm(y)
+    assert np.linalg.norm(got - y) <= HALF[elem] * norm or norm == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,K,N", [
+    (1, 16, 1), (1, 128, 16), (1, 4096, 272), (2, 144, 7), (15, 272, 33), (16, 400, 130), (17, 1040, 48), (33, 128, 200),
+    (64, 640, 64), (65, 2064, 100), (128, 512, 256), (130, 384, 129), (200, 1152, 520), (257, 256, 300), (300, 144, 16),
+    (520, 528, 272)])
+def test_layer(M, K, N, kind):
+    rng = np.random.default_rng(M + K + N)
+    for exact in (True, False):
+        for elem in TYPES:
+            x, w = operand((M, K), (M, up(K)), kind, rng, exact), operand((N, K), (up(N), up(K)), kind, rng, exact)
+            out = torch.full((M, N), MARK, dtype=TYPES[elem], device="cuda")
+            xq, xs = gpu(x)
+            wq, ws = gpu(w)
+            got = moe.moe_fp8_linear(xq, xs, wq[None], ws[None], out=out)
+            assert got.data_ptr() == out.data_ptr()
+            close(out, fp8.row_values(*x), fp8.block_values(*w), elem, exact)
+
+
+def a_plan(T, E, k, bm, rng, skew=False, elsewhere=0):
+    """The planner's outputs for random routes; with ``elsewhere`` experts that other devices hold."""
+    p = np.arange(1, E + elsewhere + 1) ** (-1.5 if skew else 0.0)
+    ids = np.stack([rng.choice(E + elsewhere, k, replace=False, p=p / p.sum()) for _ in range(T)]).astype(np.int32)
+    return moe.moe_align(torch.from_numpy(ids).cuda(), E, bm)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,E,k,bm,K,N,skew,elsewhere", [
+    (1, 4, 2, 16, 144, 40, False, 0), (30, 8, 2, 16, 512, 100, True, 0), (60, 5, 3, 32, 272, 272, False, 3),
+    (150, 6, 2, 64, 400, 130, True, 0), (200, 3, 2, 128, 384, 264, False, 2), (400, 3, 2, 256, 256, 300, True, 0),
+    (0, 4, 2, 64, 128, 64, False, 0), (90, 40, 1, 128, 144, 48, True, 0)])
+def test_plan(T, E, k, bm, K, N, skew, elsewhere, kind):
+    rng = np.random.default_rng(T + bm)
+    plan, experts, ntp = a_plan(T, E, k, bm, rng, skew, elsewhere) if T else (
+        torch.full((256,), -1, dtype=torch.int32, device="cuda"), torch.full((4,), -1, dtype=torch.int32, device="cuda"),
+        torch.zeros(1, dtype=torch.int32, device="cuda"))
+    M, n = plan.numel(), int(ntp)
+    for exact in (True, False):
+        x = operand((M, K), (M, up(K)), kind, rng, exact)
+        w = operand((E * N, K), (E * up(N), up(K)), kind, rng, exact)
+        w = w[0].reshape(E, N, K), w[1].reshape(E, up(N), up(K))
+        x[0][:n][plan.cpu().numpy()[:n] < 0] = 0
+        x[0][n:] = 0x7F  # NaN: neither read nor written
+        out = torch.full((M, N), MARK, dtype=torch.bfloat16, device="cuda")
+        moe.moe_fp8_linear(*gpu(x), *gpu(w), experts, ntp, bm, out=out)
+        assert (out[n:] == MARK).all()
+        of = experts.cpu().numpy().repeat(bm)[:M]
+        rows = np.nan_to_num(fp8.row_values(*x))
+        for e in range(E):
+            at = np.nonzero(of == e)[0]
+            if len(at):
+                close(out[torch.from_numpy(at).cuda()], rows[at], fp8.block_values(w[0][e], w[1][e]), "bf16", exact)
+        assert (of[:n] >= 0).all()
+
+
+@pytest.mark.parametrize("bm", [16, 32, 64, 128, 256])
+def test_blocks_elsewhere_give_zeros(bm):
+    rng = np.random.default_rng(bm)
+    x, w = operand((3 * bm, 128), (3 * bm, 1), "f32", rng, False), operand((2 * 64, 128), (2, 1), "f32", rng, False)
+    experts = torch.tensor([1, -1, 2], dtype=torch.int32, device="cuda")
+    ntp = torch.tensor([3 * bm], dtype=torch.int32, device="cuda")
+    wq, ws = gpu(w)
+    out = torch.full((3 * bm, 64), MARK, dtype=torch.bfloat16, device="cuda")
+    moe.moe_fp8_linear(*gpu(x), wq.reshape(2, 64, 128), ws.reshape(2, 1, 1), experts, ntp, bm, out=out)
+    assert not out[bm:].any() and (out[:bm] != MARK).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,N,K", [(0, 16, 32), (128, 1, 1), (128, 16, 16), (128, 130, 72), (256, 64, 300), (384, 257, 128),
+                                   (1280, 100, 100), (640, 256, 520)])
+def test_dw(M, N, K, kind):
+    rng = np.random.default_rng(M + N + K)
+    for exact in (True, False):
+        for elem in TYPES:
+            dy, x = operand((N, M), (N, M // 128), kind, rng, exact), operand((K, M), (K, M // 128), kind, rng, exact)
+            out = torch.full((1, N, K), MARK, dtype=TYPES[elem], device="cuda")
+            moe.moe_fp8_linear_dw(*gpu(dy), *gpu(x), out=out)
+            close(out[0], fp8.row_values(*dy), fp8.row_values(*x), elem, exact)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,E,k,bm,N,K,skew", [(1, 3, 1, 128, 16, 16, False), (300, 5, 2, 128, 72, 130, False),
+                                               (500, 12, 2, 128, 144, 64, True), (700, 3, 2, 256, 264, 300, True),
+                                               (0, 3, 1, 128, 32, 48, False)])
+def test_dw_plan(T, E, k, bm, N, K, skew, kind):
+    rng = np.random.default_rng(T + bm)
+    plan, experts, ntp = a_plan(T, E, k, bm, rng, skew) if T else (
+        torch.full((128,), -1, dtype=torch.int32, device="cuda"), torch.full((1,), -1, dtype=torch.int32, device="cuda"),
+        torch.zeros(1, dtype=torch.int32, device="cuda"))
+    M, n = up(plan.numel()) * 128, int(ntp)
+    for exact in (True, False):
+        dy, x = operand((N, M), (N, M // 128), kind, rng, exact), operand((K, M), (K, M // 128), kind, rng, exact)
+        pad = np.nonzero(plan.cpu().numpy()[:n] < 0)[0]
+        dy[0][:, pad] = 0
+        x[0][:, pad] = 0
+        dy[0][:, n:] = 0x7F  # NaN: not read
+        x[0][:, n:] = 0x7F
+        out = torch.full((E, N, K), MARK, dtype=torch.bfloat16, device="cuda")
+        moe.moe_fp8_linear_dw(*gpu(dy), *gpu(x), E, experts, ntp, bm, out=out)
+        of = np.full(M, -1)
+        of[:n] = experts.cpu().numpy().repeat(bm)[:n]
+        a, b = fp8.row_values(*dy), fp8.row_values(*x)
+        for e in range(E):
+            at = of == e
+            if at.any():
+                close(out[e], a[:, at], b[:, at], "bf16", exact)
+            else:
+                assert not out[e].any()
+
+
+def test_scales_of_nothing_and_nan():
+    # an e8m0 scale of 255 is a NaN, wherever it stands; other rows keep theirs
+    rng = np.random.default_rng(0)
+    x, w = operand((40, 256), (40, 2), "e8m0", rng, True), operand((64, 256), (1, 2), "e8m0", rng, True)
+    clean = moe.moe_fp8_linear(*gpu(x), *[v[None] for v in gpu(w)])
+    x[1][7, 1] = 255
+    out = moe.moe_fp8_linear(*gpu(x), *[v[None] for v in gpu(w)])
+    assert out[7].isnan().all()
+    keep = torch.arange(40, device="cuda") != 7
+    assert torch.equal(out[keep], clean[keep])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_same_bits_and_graph(M, kind):
+    rng = np.random.default_rng(M)
+    sets = [(gpu(operand((M, 640), (M, 5), kind, rng, False)), gpu(operand((200, 640), (2, 5), kind, rng, False)),
+             gpu(operand((48, 384), (48, 3), kind, rng, False)), gpu(operand((80, 384), (80, 3), kind, rng, False)))
+            for _ in range(3)]
+    held = [tuple(v.clone() for v in pair) for pair in sets[0]]
+    out = torch.empty(M, 200, dtype=torch.bfloat16, device="cuda")
+    g = torch.empty(1, 48, 80, dtype=torch.bfloat16, device="cuda")
+
+    def call(h=held, o=out, d=g):
+        moe.moe_fp8_linear(*h[0], *[v[None] for v in h[1]], out=o)
+        moe.moe_fp8_linear_dw(*h[2], *h[3], out=d)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for new in sets[1:] + sets[:1]:
+        for h, v in zip(held, new):
+            for a, b in zip(h, v):
+                a.view(torch.uint8).copy_(b.view(torch.uint8))
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = out.clone(), g.clone()
+        call(new, out, g)
+        assert torch.equal(a, out) and torch.equal(b, g)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    o = moe.moe_fp8_linear(*sets[0][0], *[v[None] for v in sets[0][1]], stream=s)
+    s.synchronize()
+    assert torch.equal(o, out)
