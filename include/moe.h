@@ -784,7 +784,7 @@ int moe_fp8_quant_weights(int32_t elem, int32_t scale_type, const void* w, int64
 
 /* out[m] = W[e] . x[m], out (M, N) of elem (MOE_ELEM_BF16 or MOE_ELEM_F16): x (M,
  * K) and w (E, N, K) e4m3, x_scale (M, ceil(K / 128)), w_scale (E, ceil(N / 128),
- * ceil(K / 128)); K a multiple of 16.
+ * ceil(K / 128)); K a multiple of 16, at most 2^22.
  * expert_ids NULL: one layer (E = 1).  Else the planner's expert_ids for blocks of
  * block_m rows (ceil(M / block_m) of them), and the rows are the plan's, below
  * num_tokens_post_padded; a block whose id is outside [0, E) gives zeros. */
@@ -796,7 +796,7 @@ int moe_fp8_linear(int32_t elem, int32_t scale_type, const void* x, const void* 
 /* Gradient of moe_fp8_linear's weights: dw (E, N, K)[e] = sum of d_out[m]^T x[m]
  * over the expert's rows, of elem (MOE_ELEM_BF16 or MOE_ELEM_F16), from both
  * quantized along the rows: dyt (N, M) and xt (K, M) e4m3, M a multiple of 128
- * (moe_fp8_quant's qt), scales (N, M / 128) and (K, M / 128).
+ * and at most 2^22 (moe_fp8_quant's qt), scales (N, M / 128) and (K, M / 128).
  * expert_ids NULL: one layer (E = 1), all M rows.  Else the plan's n_blocks ids
  * for blocks of block_m = 128 or 256 rows, an expert's in one run, as the planner
  * lays them out; an expert without rows gets zeros.  Padding rows must be zeros

@@ -7,6 +7,7 @@ namespace {
 
 constexpr int64_t kMaxSize = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxY = 65535;              // workgroups along a grid's second and third axis
+constexpr int64_t kMaxContraction = int64_t(1) << 22;  // 256 rows of bytes: offsets of 32 bits
 constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;  // of one launch
 
 int check_size(const char* name, int64_t n, int64_t least, int64_t multiple = 1) {
@@ -83,6 +84,7 @@ int moe_fp8_linear(int32_t elem, int32_t scale_type, const void* x, const void* 
   if ((rc = check_size("M", M, 0))) return rc;
   if ((rc = check_size("K", K, 16, 16))) return rc;
   if ((rc = check_size("N", N, 1))) return rc;
+  if (K > kMaxContraction) return abi_fail(MOE_ERR_UNSUPPORTED, "K must be at most 2^22");
   if (E < 1) return abi_fail(MOE_ERR_SHAPE, "E must be >= 1 (got %d)", E);
   if (!expert_ids && E != 1)
     return abi_fail(MOE_ERR_SHAPE, "without expert_ids there is one expert (got E = %d)", E);
@@ -109,6 +111,7 @@ int moe_fp8_linear_dw(int32_t elem, int32_t scale_type, const void* dyt, const v
   if ((rc = check_size("M", M, 0, 128))) return rc;
   if ((rc = check_size("N", N, 1))) return rc;
   if ((rc = check_size("K", K, 1))) return rc;
+  if (M > kMaxContraction) return abi_fail(MOE_ERR_UNSUPPORTED, "M must be at most 2^22");
   if (E < 1) return abi_fail(MOE_ERR_SHAPE, "E must be >= 1 (got %d)", E);
   if (!expert_ids && E != 1)
     return abi_fail(MOE_ERR_SHAPE, "without expert_ids there is one expert (got E = %d)", E);

@@ -198,6 +198,244 @@ k_fp8_rows(Fp8Args a) {
   }
 }
 
+// ---- many rows: tiles staged in LDS ------------------------------------------
+//
+// A workgroup computes BM rows of X by BN rows of W; a wave TM x 64 of them.  One
+// 128-wide step of both operands is a stage of LDS, brought there by direct loads
+// NS - 1 steps ahead.  LDS rows are 128 bytes, chunk q of a row stored at q ^ key
+// so that the 16 rows of a fragment read spread over the banks.
+//
+// A wave's four subtiles of W interleave: row r of subtile s is W's row 16 (r / 4) +
+// 4 s + r % 4 of the wave's 64, so that a lane ends with 16 consecutive n of one row.
+constexpr int kRow = 128;
+constexpr uint32_t kOut = 0xC0000000u;  // an offset past every buffer: loads zeros
+
+__device__ __forceinline__ int x_key(int r) { return r & 7; }
+__device__ __forceinline__ int w_key(int r) { return (r & 3) | ((r >> 4) & 1) << 2; }
+
+template <int BM, int BN, int TM, int NS, int SCALE, bool DW>
+struct Tile {
+  static constexpr int MI = TM / 16, NI = 4;
+  static constexpr int WN = BN / 64, WM = BM / TM, NW = WM * WN;
+  static constexpr int X = BM * kRow, W = BN * kRow;
+  static constexpr int SX = SCALE == SCALE_F32 ? BM * 4 : 0;  // row scales of a stage
+  static constexpr int SW = SCALE == SCALE_F32 && DW ? BN * 4 : 0;
+  static constexpr int STAGE = X + W + SX + SW;
+  static constexpr int XI = X / 1024 / NW, WI = W / 1024 / NW;  // 16-byte loads a wave and stage
+  static constexpr int SI = (SX + SW) / 256;                    // 4-byte loads, one a wave
+  static_assert(X % (1024 * NW) == 0 && W % (1024 * NW) == 0 && SI <= NW);
+  static constexpr int THREADS = NW * 64;
+};
+
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS reads are done
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Four steps' e8m0 scales from byte i on; n bytes in all (at least four).
+__device__ __forceinline__ uint32_t scales4(const uint8_t* p, int64_t i, int64_t n) {
+  typedef uint32_t u32_any __attribute__((aligned(1)));
+  const int64_t at = i + 4 <= n ? i : n - 4;
+  return *reinterpret_cast<const u32_any*>(p + at) >> (8 * (int)(i - at));
+}
+
+template <int OELEM, int SCALE, bool DW, int BM, int BN, int TM, int NS>
+__global__ void __launch_bounds__((Tile<BM, BN, TM, NS, SCALE, DW>::THREADS))
+k_fp8_tiles(Fp8Args a, int mtiles, int ntiles) {
+  using C = Tile<BM, BN, TM, NS, SCALE, DW>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * C::STAGE];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int g = lane >> 4, r16 = lane & 15;
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  // consecutive tiles on one XCD; groups of four row tiles walk the columns together
+  int valid = mtiles;
+  if (!DW && a.experts) valid = min((min(max(*a.ntp, 0), (int)a.M) + BM - 1) / BM, mtiles);
+  const int total = valid * ntiles;
+  const int per = (total + 7) / 8, j = blockIdx.x / 8;
+  const int tile = (blockIdx.x % 8) * per + j;
+  if (j >= per || tile >= total) return;
+  const int band = tile / (4 * ntiles), inb = tile - band * 4 * ntiles;
+  const int tall = min(4, valid - 4 * band);
+  const int mt = 4 * band + inb % tall, nt = inb / tall;
+  const Part p = part_of<DW>(a, mt, BM, blockIdx.y);
+  if (p.none) return;
+  const int64_t n0 = (int64_t)nt * BN;
+  const int wrows = (int)min((int64_t)BN, a.N - n0);
+  const int64_t K = a.K, GK = (K + 127) / 128;
+  const int64_t we = DW ? 0 : max(p.e, 0);
+  const int steps = p.e < 0 ? 0 : (int)((p.k1 - p.k0 + 127) / 128);
+  const int tail = (int)(p.k1 - p.k0) & 127;  // bytes of a last step that is not whole
+
+  const desc_t rx = make_desc(a.x + p.m0 * K + p.k0, (uint32_t)(p.rows * K - p.k0));
+  const desc_t rw = make_desc(a.w + (we * a.N + n0) * K + p.k0, (uint32_t)(wrows * K - p.k0));
+  uint32_t xo[C::XI], wo[C::WI];
+  bool xt[C::XI], wt[C::WI];  // this lane's chunk lies behind the tail
+#pragma unroll
+  for (int t = 0; t < C::XI; ++t) {
+    const int slot = (wave + C::NW * t) * 64 + lane, row = slot / 8, q = (slot % 8) ^ x_key(row);
+    xo[t] = (uint32_t)row * (uint32_t)K + q * 16;
+    xt[t] = q * 16 >= tail;
+  }
+#pragma unroll
+  for (int t = 0; t < C::WI; ++t) {
+    const int slot = (wave + C::NW * t) * 64 + lane, row = slot / 8, q = (slot % 8) ^ w_key(row);
+    wo[t] = (uint32_t)row * (uint32_t)K + q * 16;
+    wt[t] = q * 16 >= tail;
+  }
+  const uint32_t lds0 = lds_addr(smem);
+  // row scales: wave w brings rows [64 w, 64 w + 64) of X, then of W
+  desc_t rs = rx;
+  uint32_t so = 0;
+  if constexpr (SCALE == SCALE_F32) {
+    constexpr int XS = C::SX / 256;
+    const bool isx = wave < XS;
+    const int64_t first = isx ? p.m0 : n0;
+    const int rows = isx ? p.rows : wrows;
+    rs = make_desc(static_cast<const float*>(isx ? a.xs : a.ws) + first * GK, (uint32_t)(rows * GK * 4));
+    so = (uint32_t)((isx ? wave : wave - XS) * 64 + lane) * (uint32_t)(GK * 4);
+  }
+  const uint32_t g0 = (uint32_t)(p.k0 / 128);
+  auto load = [&](int i) {
+    const uint32_t st = lds0 + (uint32_t)(i % NS) * C::STAGE, k = (uint32_t)i * kRow;
+    const bool cut = tail && i == steps - 1;
+#pragma unroll
+    for (int t = 0; t < C::XI; ++t) dma16(rx, st + (wave + C::NW * t) * 1024, cut && xt[t] ? kOut : xo[t], k);
+#pragma unroll
+    for (int t = 0; t < C::WI; ++t)
+      dma16(rw, st + C::X + (wave + C::NW * t) * 1024, cut && wt[t] ? kOut : wo[t], k);
+    if constexpr (SCALE == SCALE_F32)
+      if (wave < C::SI) dma4(rs, st + C::X + C::W + wave * 256, so, (g0 + i) * 4);
+  };
+  f32x4 acc[C::MI][C::NI];
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // e8m0: four steps' scales of this lane's rows, and the next four's, requested in
+  // the fourth step ahead of its operand loads (a wait for them after those
+  // would wait for those too)
+  uint32_t ex[C::MI], ew[C::NI], exn[C::MI], ewn[C::NI];
+  auto load_e8 = [&](int i) {
+    const int64_t gk = g0 + i;
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi) {
+      const int64_t m = min(p.m0 + wm * TM + 16 * mi + r16, a.M - 1);
+      exn[mi] = scales4(static_cast<const uint8_t*>(a.xs), m * GK + gk, a.M * GK);
+    }
+    if constexpr (DW) {
+#pragma unroll
+      for (int ni = 0; ni < C::NI; ++ni) {
+        const int64_t n = min(n0 + wn * 64 + (r16 >> 2) * 16 + ni * 4 + (r16 & 3), a.N - 1);
+        ewn[ni] = scales4(static_cast<const uint8_t*>(a.ws), n * GK + gk, a.N * GK);
+      }
+    } else {
+      const int64_t NB = (a.N + 127) / 128, nb = min((n0 + wn * 64) / 128, NB - 1);
+      ewn[0] = scales4(static_cast<const uint8_t*>(a.ws), (we * NB + nb) * GK + gk, a.E * NB * GK);
+    }
+  };
+  const float* wsc = nullptr;  // fp32 layer: the scales of the wave's block of W
+  if constexpr (SCALE == SCALE_F32 && !DW) {
+    const int64_t NB = (a.N + 127) / 128, nb = min((n0 + wn * 64) / 128, NB - 1);
+    wsc = static_cast<const float*>(a.ws) + (we * NB + nb) * GK;
+  }
+
+  if constexpr (SCALE == SCALE_E8M0)
+    if (steps) load_e8(0);
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i)
+    if (i < steps) load(i);
+  for (int i = 0; i < steps; ++i) {
+    wait_vmcnt<0>();
+    lds_barrier();
+    if constexpr (SCALE == SCALE_E8M0) {
+      if ((i & 3) == 0) {
+#pragma unroll
+        for (int mi = 0; mi < C::MI; ++mi) ex[mi] = exn[mi];
+#pragma unroll
+        for (int ni = 0; ni < (DW ? C::NI : 1); ++ni) ew[ni] = ewn[ni];
+      }
+      if ((i & 3) == 3 && i + 1 < steps) load_e8(i + 1);
+    }
+    if (i + NS - 1 < steps) load(i + NS - 1);
+    const uint8_t* st = smem + (i % NS) * C::STAGE;
+    Frag<KIND_FP8B> fw[C::NI];
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ++ni) {
+      const int row = wn * 64 + (r16 >> 2) * 16 + ni * 4 + (r16 & 3);
+      const uint8_t* q = st + C::X + row * kRow;
+      fw[ni].c[0] = *reinterpret_cast<const uint4*>(q + ((g ^ w_key(row)) << 4));
+      fw[ni].c[1] = *reinterpret_cast<const uint4*>(q + (((4 + g) ^ w_key(row)) << 4));
+    }
+    float sw[C::NI][4];
+    if constexpr (SCALE == SCALE_F32) {
+      if constexpr (DW) {
+        const float* q = reinterpret_cast<const float*>(st + C::X + C::W + C::SX);
+#pragma unroll
+        for (int ni = 0; ni < C::NI; ++ni)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sw[ni][c] = q[wn * 64 + g * 16 + ni * 4 + c];
+      } else {
+        sw[0][0] = wsc[i];
+      }
+    }
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi) {
+      const int row = wm * TM + 16 * mi + r16;
+      const uint8_t* q = st + row * kRow;
+      Frag<KIND_FP8B> fx;
+      fx.c[0] = *reinterpret_cast<const uint4*>(q + ((g ^ x_key(row)) << 4));
+      fx.c[1] = *reinterpret_cast<const uint4*>(q + (((4 + g) ^ x_key(row)) << 4));
+      if constexpr (SCALE == SCALE_F32) {
+        float sx = reinterpret_cast<const float*>(st + C::X + C::W)[row];
+        if constexpr (!DW) sx *= sw[0][0];
+#pragma unroll
+        for (int ni = 0; ni < C::NI; ++ni) {
+          const f32x4 d = mfma_step<KIND_FP8B>(fw[ni], fx, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            acc[mi][ni][c] = __builtin_fmaf(d[c], DW ? sx * sw[ni][c] : sx, acc[mi][ni][c]);
+        }
+      } else {
+#pragma unroll
+        for (int ni = 0; ni < C::NI; ++ni)
+          acc[mi][ni] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              as_i32x8(fw[ni].c[0], fw[ni].c[1]), as_i32x8(fx.c[0], fx.c[1]), acc[mi][ni], 0, 0, 0,
+              (int)ew[DW ? ni : 0], 0, (int)ex[mi]);
+        ex[mi] >>= 8;
+      }
+    }
+    if constexpr (SCALE == SCALE_E8M0) {
+#pragma unroll
+      for (int ni = 0; ni < (DW ? C::NI : 1); ++ni) ew[ni] >>= 8;
+    }
+  }
+  // a lane: row m, 16 consecutive n
+  const int64_t n = n0 + wn * 64 + g * 16;
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi) {
+    const int m = wm * TM + 16 * mi + r16;
+    if (m >= p.rows) continue;
+    uint16_t* o = static_cast<uint16_t*>(a.out) + ((DW ? p.e * a.M : 0) + p.m0 + m) * a.N + n;
+    uint32_t v[8];
+#pragma unroll
+    for (int ni = 0; ni < 4; ++ni)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        v[2 * ni + c] = to_elem<OELEM>(acc[mi][ni][2 * c]) | to_elem<OELEM>(acc[mi][ni][2 * c + 1]) << 16;
+    if ((a.N & 7) == 0 && n + 16 <= a.N) {
+      reinterpret_cast<uint4*>(o)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<uint4*>(o)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        if (n + c < a.N) o[c] = (uint16_t)(c & 1 ? v[c / 2] >> 16 : v[c / 2]);
+    }
+  }
+}
+
 template <class F>
 void by_types(const Fp8Args& a, F f) {
   auto with = [&](auto OELEM) {
@@ -215,15 +453,35 @@ void rows_kernel(const Fp8Args& a, hipStream_t stream) {
   hipLaunchKernelGGL((k_fp8_rows<OELEM, SCALE, NT, DW>), grid, dim3(kW * 64), 0, stream, a);
 }
 
+template <int OELEM, int SCALE, bool DW, int BM, int BN, int TM, int NS>
+void tile_kernel(const Fp8Args& a, hipStream_t stream) {
+  const int mt = (int)((a.M + BM - 1) / BM), nt = (int)((a.N + BN - 1) / BN);
+  const unsigned tiles = ((unsigned)(mt * nt) + 7) / 8 * 8;
+  hipLaunchKernelGGL((k_fp8_tiles<OELEM, SCALE, DW, BM, BN, TM, NS>), dim3(tiles, (unsigned)(DW ? a.E : 1)),
+                     dim3(Tile<BM, BN, TM, NS, SCALE, DW>::THREADS), 0, stream, a, mt, nt);
+}
+
 }  // namespace
 
 hipError_t launch_fp8_linear(const Fp8Args& a, hipStream_t stream) {
   if (a.M == 0) return hipSuccess;
   by_types(a, [&](auto OELEM, auto SCALE) {
-    if (a.dw) rows_kernel<OELEM(), SCALE(), 4, true>(a, stream);
-    else if (a.experts ? a.block_m == 16 : a.M <= 16) rows_kernel<OELEM(), SCALE(), 1, false>(a, stream);
-    else if (a.experts ? a.block_m == 32 : a.M <= 32) rows_kernel<OELEM(), SCALE(), 2, false>(a, stream);
-    else rows_kernel<OELEM(), SCALE(), 4, false>(a, stream);
+    constexpr int O = OELEM(), S = SCALE();
+    const int64_t rows = a.experts && !a.dw ? a.block_m : a.M;
+    if (a.dw) {
+      if (a.M > 64 && a.N > 64) tile_kernel<O, S, true, 256, 256, 128, 2>(a, stream);
+      else rows_kernel<O, S, 4, true>(a, stream);
+    } else if (rows <= 16) {
+      rows_kernel<O, S, 1, false>(a, stream);
+    } else if (rows <= 32) {
+      rows_kernel<O, S, 2, false>(a, stream);
+    } else if (rows <= 64) {
+      rows_kernel<O, S, 4, false>(a, stream);
+    } else if (rows <= 128) {
+      tile_kernel<O, S, false, 128, 128, 64, 2>(a, stream);
+    } else {
+      tile_kernel<O, S, false, 256, 256, 128, 2>(a, stream);
+    }
   });
   return hipGetLastError();
 }

@@ -58,6 +58,7 @@ def test_outputs_are_16_bits():
     (linear, dict(E=2), SHAPE), (linear, dict(N=1 << 21), UNSUPPORTED), (linear, dict(M=1 << 26, N=1 << 19), UNSUPPORTED),
     (linear, {**PLAN, "bm": 48}, UNSUPPORTED), (linear, {**PLAN, "bm": 0}, UNSUPPORTED), (linear, {**PLAN, "ntp": None}, NULL),
     (linear, {**PLAN, "ntp": P((1 << 20) + 2)}, ALIGN),
+    (linear, dict(K=(1 << 22) + 16), UNSUPPORTED), (dw, dict(M=(1 << 22) + 128), UNSUPPORTED),
     (dw, dict(M=-128), SHAPE), (dw, dict(M=64), SHAPE), (dw, dict(N=0), SHAPE), (dw, dict(K=0), SHAPE), (dw, dict(E=0), SHAPE),
     (dw, dict(E=2), SHAPE), (dw, {**PLAN, "bm": 64}, UNSUPPORTED), (dw, {**PLAN, "nb": -1}, SHAPE),
     (dw, {**PLAN, "ntp": None}, NULL), (dw, dict(N=1 << 26, K=1 << 19), UNSUPPORTED)])
