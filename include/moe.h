@@ -799,8 +799,8 @@ int moe_fp8_linear(int32_t elem, int32_t scale_type, const void* x, const void* 
  * and at most 2^22 (moe_fp8_quant's qt), scales (N, M / 128) and (K, M / 128).
  * expert_ids NULL: one layer (E = 1), all M rows.  Else the plan's n_blocks ids
  * for blocks of block_m = 128 or 256 rows, an expert's in one run, as the planner
- * lays them out; an expert without rows gets zeros.  Padding rows must be zeros
- * (moe_permute writes them so).  M == 0 writes zeros. */
+ * lays them out (E <= 1024); an expert without rows gets zeros.  Padding rows must
+ * be zeros (moe_permute writes them so).  M == 0 writes zeros. */
 int moe_fp8_linear_dw(int32_t elem, int32_t scale_type, const void* dyt, const void* dyt_scale,
                       const void* xt, const void* xt_scale, const int32_t* expert_ids,
                       const int32_t* num_tokens_post_padded, void* dw, int64_t M, int64_t N, int64_t K,

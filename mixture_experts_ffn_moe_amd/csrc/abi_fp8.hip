@@ -118,6 +118,8 @@ int moe_fp8_linear_dw(int32_t elem, int32_t scale_type, const void* dyt, const v
   if (expert_ids && block_m != 128 && block_m != 256)
     return abi_fail(MOE_ERR_UNSUPPORTED,
                     "block_m must be 128 or 256, so that a scale's rows are one expert's (got %d)", block_m);
+  if (expert_ids && E > kFp8MaxPlanExperts)
+    return abi_fail(MOE_ERR_UNSUPPORTED, "a plan's gradient supports E <= %d (got %d)", kFp8MaxPlanExperts, E);
   if (expert_ids && (rc = check_size("n_blocks", n_blocks, 0))) return rc;
   if (E > kMaxY || up(K, 16) > kMaxY || up(N, 16) * 512 > kMaxThreads / up(K, 16) / E)
     return abi_fail(MOE_ERR_UNSUPPORTED, "E * N * K is too large for one launch");

@@ -130,4 +130,5 @@ struct Fp8Args {
   int E, block_m, n_blocks;
   int oelem, scale_type, dw;
 };
+constexpr int kFp8MaxPlanExperts = 1024;  // of a gradient over a plan
 hipError_t launch_fp8_linear(const Fp8Args& a, hipStream_t stream);

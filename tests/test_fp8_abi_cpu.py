@@ -60,7 +60,7 @@ def test_outputs_are_16_bits():
     (linear, {**PLAN, "ntp": P((1 << 20) + 2)}, ALIGN),
     (linear, dict(K=(1 << 22) + 16), UNSUPPORTED), (dw, dict(M=(1 << 22) + 128), UNSUPPORTED),
     (dw, dict(M=-128), SHAPE), (dw, dict(M=64), SHAPE), (dw, dict(N=0), SHAPE), (dw, dict(K=0), SHAPE), (dw, dict(E=0), SHAPE),
-    (dw, dict(E=2), SHAPE), (dw, {**PLAN, "bm": 64}, UNSUPPORTED), (dw, {**PLAN, "nb": -1}, SHAPE),
+    (dw, dict(E=2), SHAPE), (dw, {**PLAN, "bm": 64}, UNSUPPORTED), (dw, {**PLAN, "E": 1025}, UNSUPPORTED), (dw, {**PLAN, "nb": -1}, SHAPE),
     (dw, {**PLAN, "ntp": None}, NULL), (dw, dict(N=1 << 26, K=1 << 19), UNSUPPORTED)])
 def test_sizes(call, bad, status):
     assert call(**bad) == status

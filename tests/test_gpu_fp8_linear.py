@@ -63,7 +63,7 @@ def close(out, x, w, elem, exact):
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M,K,N", [
     (1, 16, 1), (1, 128, 16), (1, 4096, 272), (2, 144, 7), (15, 272, 33), (16, 400, 130), (17, 1040, 48), (33, 128, 200),
-    (64, 640, 64), (65, 2064, 100), (128, 512, 256), (130, 384, 129), (200, 1152, 520), (257, 256, 300), (300, 144, 16),
+    (64, 640, 64), (65, 2064, 100), (128, 512, 256), (130, 384, 129), (200, 1152, 520), (257, 256, 300), (4200, 272, 1032), (1100, 128, 4500), (300, 144, 16),
     (520, 528, 272)])
 def test_layer(M, K, N, kind):
     rng = np.random.default_rng(M + K + N)
@@ -89,7 +89,8 @@ def a_plan(T, E, k, bm, rng, skew=False, elsewhere=0):
 @pytest.mark.parametrize("T,E,k,bm,K,N,skew,elsewhere", [
     (1, 4, 2, 16, 144, 40, False, 0), (30, 8, 2, 16, 512, 100, True, 0), (60, 5, 3, 32, 272, 272, False, 3),
     (150, 6, 2, 64, 400, 130, True, 0), (200, 3, 2, 128, 384, 264, False, 2), (400, 3, 2, 256, 256, 300, True, 0),
-    (0, 4, 2, 64, 128, 64, False, 0), (90, 40, 1, 128, 144, 48, True, 0)])
+    (0, 4, 2, 64, 128, 64, False, 0), (90, 40, 1, 128, 144, 48, True, 0), (2000, 3, 2, 128, 128, 272, True, 1),
+    (900, 70, 2, 128, 128, 520, True, 5)])
 def test_plan(T, E, k, bm, K, N, skew, elsewhere, kind):
     rng = np.random.default_rng(T + bm)
     plan, experts, ntp = a_plan(T, E, k, bm, rng, skew, elsewhere) if T else (
@@ -126,9 +127,46 @@ def test_blocks_elsewhere_give_zeros(bm):
     assert not out[bm:].any() and (out[:bm] != MARK).all()
 
 
+def test_any_order_of_blocks():
+    # runs of one expert, blocks alone, elsewhere, the same expert again; a last block cut by the rows in use
+    rng = np.random.default_rng(3)
+    order, bm = [2, 2, 2, 0, 2, -1, 1, 1, 1, 1, 1, 5, 5, 0, 0], 128
+    M, K, N = len(order) * bm, 144, 264
+    for kind in KINDS:
+        x, w = operand((M, K), (M, 2), kind, rng, True), operand((3 * N, K), (3 * up(N), 2), kind, rng, True)
+        w = w[0].reshape(3, N, K), w[1].reshape(3, up(N), 2)
+        out = torch.full((M, N), MARK, dtype=torch.bfloat16, device="cuda")
+        n = M - 40
+        moe.moe_fp8_linear(*gpu(x), *gpu(w), torch.tensor(order, dtype=torch.int32, device="cuda"),
+                           torch.tensor([n], dtype=torch.int32, device="cuda"), bm, out=out)
+        rows = fp8.row_values(*x)
+        for b, e in enumerate(order):
+            at = slice(b * bm, min((b + 1) * bm, n))
+            if 0 <= e < 3:
+                close(out[at], rows[at], fp8.block_values(w[0][e], w[1][e]), "bf16", True)
+            else:
+                assert not out[at].any()
+        assert (out[n:] == MARK).all()
+
+
+@pytest.mark.parametrize("blocks", [4095, 4096, 4097, 5000])
+def test_many_blocks(blocks):
+    # more row tiles than the kernel keeps a list of: each block is a tile then
+    rng = np.random.default_rng(blocks)
+    bm, K, N, E = 128, 16, 24, 7
+    ids = np.sort(rng.integers(0, E, blocks)).astype(np.int32)
+    q = torch.randint(0, 2, (blocks * bm, K), device="cuda").float().to(torch.float8_e4m3fn)
+    s = torch.ones(blocks * bm, 1, device="cuda")
+    w = torch.arange(E, device="cuda").float()[:, None, None].expand(E, N, K).contiguous().to(torch.float8_e4m3fn)
+    out = moe.moe_fp8_linear(q, s, w, torch.ones(E, 1, 1, device="cuda"), torch.from_numpy(ids).cuda(),
+                             torch.tensor([blocks * bm], dtype=torch.int32, device="cuda"), bm)
+    want = q.float().sum(1) * torch.from_numpy(ids).cuda().repeat_interleave(bm)
+    assert torch.equal(out.float(), want[:, None].expand(-1, N))
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M,N,K", [(0, 16, 32), (128, 1, 1), (128, 16, 16), (128, 130, 72), (256, 64, 300), (384, 257, 128),
-                                   (1280, 100, 100), (640, 256, 520)])
+                                   (1280, 100, 100), (640, 256, 520), (256, 4400, 1100)])
 def test_dw(M, N, K, kind):
     rng = np.random.default_rng(M + N + K)
     for exact in (True, False):
@@ -141,7 +179,7 @@ def test_dw(M, N, K, kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("T,E,k,bm,N,K,skew", [(1, 3, 1, 128, 16, 16, False), (300, 5, 2, 128, 72, 130, False),
-                                               (500, 12, 2, 128, 144, 64, True), (700, 3, 2, 256, 264, 300, True),
+                                               (500, 12, 2, 128, 144, 64, True), (300, 60, 2, 128, 520, 264, True), (700, 3, 2, 256, 264, 300, True),
                                                (0, 3, 1, 128, 32, 48, False)])
 def test_dw_plan(T, E, k, bm, N, K, skew, kind):
     rng = np.random.default_rng(T + bm)
