@@ -90,7 +90,8 @@ int moe_fp8_linear(int32_t elem, int32_t scale_type, const void* x, const void* 
     return abi_fail(MOE_ERR_SHAPE, "without expert_ids there is one expert (got E = %d)", E);
   if (expert_ids && block_m != 16 && block_m != 32 && block_m != 64 && block_m != 128 && block_m != 256)
     return abi_fail(MOE_ERR_UNSUPPORTED, "block_m must be 16, 32, 64, 128 or 256 (got %d)", block_m);
-  if (up(N, 16) > kMaxY || up(M, 16) * 512 > kMaxThreads / up(N, 16))
+  const bool few = (expert_ids ? block_m : M) <= 32;  // a workgroup for each 16 rows of weights
+  if (few ? up(M, 16) * 512 > kMaxThreads / up(N, 16) : up(M, 64) > kMaxSize / up(N, 64))
     return abi_fail(MOE_ERR_UNSUPPORTED, "M * N is too large for one launch");
   if ((rc = check_ntp(num_tokens_post_padded, expert_ids != nullptr))) return rc;
   if ((rc = check_ptrs({{x, M > 0}, {x_scale, M > 0}, {w, M > 0}, {w_scale, M > 0}, {expert_ids, false},
@@ -121,7 +122,7 @@ int moe_fp8_linear_dw(int32_t elem, int32_t scale_type, const void* dyt, const v
   if (expert_ids && E > kFp8MaxPlanExperts)
     return abi_fail(MOE_ERR_UNSUPPORTED, "a plan's gradient supports E <= %d (got %d)", kFp8MaxPlanExperts, E);
   if (expert_ids && (rc = check_size("n_blocks", n_blocks, 0))) return rc;
-  if (E > kMaxY || up(K, 16) > kMaxY || up(N, 16) * 512 > kMaxThreads / up(K, 16) / E)
+  if (up(N, 64) > kMaxSize / up(K, 64) / E)
     return abi_fail(MOE_ERR_UNSUPPORTED, "E * N * K is too large for one launch");
   if ((rc = check_ntp(num_tokens_post_padded, expert_ids != nullptr))) return rc;
   if ((rc = check_ptrs({{dyt, M > 0}, {dyt_scale, M > 0}, {xt, M > 0}, {xt_scale, M > 0},

@@ -55,13 +55,14 @@ def test_outputs_are_16_bits():
     (weights, dict(E=-1), SHAPE), (weights, dict(N=0), SHAPE), (weights, dict(N=24), SHAPE), (weights, dict(K=8), SHAPE),
     (weights, dict(E=1 << 16), UNSUPPORTED), (weights, dict(N=1 << 24), UNSUPPORTED),
     (linear, dict(M=-1), SHAPE), (linear, dict(K=8), SHAPE), (linear, dict(N=0), SHAPE), (linear, dict(E=0), SHAPE),
-    (linear, dict(E=2), SHAPE), (linear, dict(N=1 << 21), UNSUPPORTED), (linear, dict(M=1 << 26, N=1 << 19), UNSUPPORTED),
+    (linear, dict(E=2), SHAPE), (linear, dict(N=1 << 27), UNSUPPORTED), (linear, dict(M=1 << 26, N=1 << 19), UNSUPPORTED),
+    (linear, dict(M=1 << 23, N=1 << 12, **{**PLAN, 'bm': 16}), UNSUPPORTED),
     (linear, {**PLAN, "bm": 48}, UNSUPPORTED), (linear, {**PLAN, "bm": 0}, UNSUPPORTED), (linear, {**PLAN, "ntp": None}, NULL),
     (linear, {**PLAN, "ntp": P((1 << 20) + 2)}, ALIGN),
     (linear, dict(K=(1 << 22) + 16), UNSUPPORTED), (dw, dict(M=(1 << 22) + 128), UNSUPPORTED),
     (dw, dict(M=-128), SHAPE), (dw, dict(M=64), SHAPE), (dw, dict(N=0), SHAPE), (dw, dict(K=0), SHAPE), (dw, dict(E=0), SHAPE),
     (dw, dict(E=2), SHAPE), (dw, {**PLAN, "bm": 64}, UNSUPPORTED), (dw, {**PLAN, "E": 1025}, UNSUPPORTED), (dw, {**PLAN, "nb": -1}, SHAPE),
-    (dw, {**PLAN, "ntp": None}, NULL), (dw, dict(N=1 << 26, K=1 << 19), UNSUPPORTED)])
+    (dw, {**PLAN, "ntp": None}, NULL), (dw, dict(N=1 << 26, K=1 << 19), UNSUPPORTED), (dw, dict(N=1 << 23, K=1 << 17, **{**PLAN, 'E': 128}), UNSUPPORTED)])
 def test_sizes(call, bad, status):
     assert call(**bad) == status
 

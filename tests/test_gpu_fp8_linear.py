@@ -63,7 +63,8 @@ def close(out, x, w, elem, exact):
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M,K,N", [
     (1, 16, 1), (1, 128, 16), (1, 4096, 272), (2, 144, 7), (15, 272, 33), (16, 400, 130), (17, 1040, 48), (33, 128, 200),
-    (64, 640, 64), (65, 2064, 100), (128, 512, 256), (130, 384, 129), (200, 1152, 520), (257, 256, 300), (4200, 272, 1032), (1100, 128, 4500), (300, 144, 16),
+    (64, 640, 64), (65, 2064, 100), (128, 512, 256), (130, 384, 129), (200, 1152, 520), (257, 256, 300), (4200, 272, 1032), (1100, 128, 4500),
+    (9, 272, 9000), (32, 400, 20000), (40, 1040, 1000), (150, 1296, 5000), (1030, 144, 1500), (3000, 144, 3500), (300, 144, 16),
     (520, 528, 272)])
 def test_layer(M, K, N, kind):
     rng = np.random.default_rng(M + K + N)
@@ -149,7 +150,7 @@ def test_any_order_of_blocks():
         assert (out[n:] == MARK).all()
 
 
-@pytest.mark.parametrize("blocks", [4095, 4096, 4097, 5000])
+@pytest.mark.parametrize("blocks", [2047, 2048, 2049, 3000])
 def test_many_blocks(blocks):
     # more row tiles than the kernel keeps a list of: each block is a tile then
     rng = np.random.default_rng(blocks)
@@ -166,7 +167,7 @@ def test_many_blocks(blocks):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M,N,K", [(0, 16, 32), (128, 1, 1), (128, 16, 16), (128, 130, 72), (256, 64, 300), (384, 257, 128),
-                                   (1280, 100, 100), (640, 256, 520), (256, 4400, 1100)])
+                                   (1280, 100, 100), (640, 256, 520), (256, 4400, 1100), (128, 1500, 1400), (128, 3000, 2500)])
 def test_dw(M, N, K, kind):
     rng = np.random.default_rng(M + N + K)
     for exact in (True, False):
