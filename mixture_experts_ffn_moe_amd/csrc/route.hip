@@ -11,6 +11,8 @@
 // within fp32's last bits of each other (8,192 tokens of 256 experts: a pair at
 // the border of the choice in about every eighth call), and a choice must not
 // depend on how a 32-bit exponential rounds.
+#include <type_traits>
+
 #include "device.h"
 #include "ops.h"
 
@@ -33,6 +35,52 @@ __device__ __forceinline__ void store_f32(void* p, int64_t i, float v) {
   else static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
 }
 
+// Four at i, a multiple of four.
+template <int ELEM>
+__device__ __forceinline__ void store4_f32(void* p, int64_t i, float4 v) {
+  if constexpr (ELEM == ELEM_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
+  } else {
+    auto bits = [](float x) -> uint32_t {
+      if constexpr (ELEM == ELEM_F16) return __builtin_bit_cast(uint16_t, (_Float16)x);
+      else return f32_to_bf16(x);
+    };
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+        make_uint2(bits(v.x) | bits(v.y) << 16, bits(v.z) | bits(v.w) << 16);
+  }
+}
+
+// The value lane movement CTRL (a DPP control) brings in.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const u64 b = __builtin_bit_cast(u64, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (u64)hi << 32 | lo);
+}
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E;         // quad_perm: lanes 1 and 2 apart
+constexpr int kMirror8 = 0x141, kMirror16 = 0x140;  // row_half_mirror, row_mirror
+
+__device__ __forceinline__ double read_f64(double v, int lane) {
+  const u64 b = __builtin_bit_cast(u64, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, (u64)hi << 32 | lo);
+}
+
+// Sum over each 16 lanes, in all of them: the pairs of mirrored lanes hold equal
+// sums of equal parts.
+__device__ __forceinline__ double sum16_f64(double v) {
+  v += dpp_f64<kSwap1>(v);
+  v += dpp_f64<kSwap2>(v);
+  v += dpp_f64<kMirror8>(v);
+  return v + dpp_f64<kMirror16>(v);
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+  v = sum16_f64(v);
+  return (read_f64(v, 0) + read_f64(v, 16)) + (read_f64(v, 32) + read_f64(v, 48));
+}
+
 __device__ __forceinline__ float wave_max_f32(float v) {
   v = wave_max16(v);
   const int i = __float_as_int(v);
@@ -43,31 +91,52 @@ __device__ __forceinline__ float wave_max_f32(float v) {
                       __int_as_float(__builtin_amdgcn_readlane(i, 48))));
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-
-// Largest 32-bit value over the wave, in a scalar register.
 template <int CTRL>
 __device__ __forceinline__ uint32_t umax_dpp(uint32_t v) {
   const uint32_t u = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
   return v > u ? v : u;
 }
+// Largest value over the wave, in a scalar register.
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-  v = umax_dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
-  v = umax_dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
-  v = umax_dpp<0x124>(v);  // row_ror 4
-  v = umax_dpp<0x128>(v);  // row_ror 8
+  v = umax_dpp<kSwap1>(v);
+  v = umax_dpp<kSwap2>(v);
+  v = umax_dpp<kMirror8>(v);
+  v = umax_dpp<kMirror16>(v);
   const uint32_t a = __builtin_amdgcn_readlane((int)v, 0), b = __builtin_amdgcn_readlane((int)v, 16);
   const uint32_t c = __builtin_amdgcn_readlane((int)v, 32), d = __builtin_amdgcn_readlane((int)v, 48);
   const uint32_t ab = a > b ? a : b, cd = c > d ? c : d;
   return ab > cd ? ab : cd;
 }
 
-// A double's bits in an order that unsigned comparison follows; 0 for none (only
-// a NaN would come out as 0).
+// e^x in 64 bits, within 2 units in the last place: x = n ln 2 + r with ln 2 in two
+// parts (Cody and Waite), the Taylor polynomial of e^r to r^13 (|r| <= ln 2 / 2: the
+// next term is below 2^-57), and 2^n.  Infinite past 709.8, 0 below -745.2; no NaN.
+__device__ __forceinline__ double exp_f64(double x) {
+  x = __builtin_fmin(__builtin_fmax(x, -800.0), 800.0);
+  const double n = __builtin_rint(x * 1.4426950408889634074);
+  double r = __builtin_fma(n, -6.93147180369123816490e-01, x);
+  r = __builtin_fma(n, -1.90821492927058770002e-10, r);
+  double p = 1.0 / 6227020800.0;
+  p = __builtin_fma(p, r, 1.0 / 479001600.0);
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+
+__device__ __forceinline__ double sigmoid_f64(float l) { return 1.0 / (1.0 + exp_f64(-(double)l)); }
+
+// A double's bits in an order that unsigned comparison follows; every number's
+// high half is above 0.
 __device__ __forceinline__ u64 order_key(double c) {
   const u64 b = __builtin_bit_cast(u64, c);
   return b ^ ((b >> 63) ? ~0ull : 0x8000000000000000ull);
@@ -79,130 +148,151 @@ __device__ __forceinline__ float clean_logit(float l) {
   return l > -INFINITY ? __builtin_fminf(l, 3.402823466e38f) : -INFINITY;
 }
 
-// One wave a token; lane holds experts lane, lane + 64, .. in NV registers.
+// (b1, b2), a lane's best two, merged with those of the lane that CTRL brings in.
+template <int CTRL>
+__device__ __forceinline__ void merge_top2(double& b1, double& b2) {
+  const double o1 = dpp_f64<CTRL>(b1), o2 = dpp_f64<CTRL>(b2);
+  b2 = __builtin_fmax(__builtin_fmin(b1, o1), __builtin_fmax(b2, o2));
+  b1 = __builtin_fmax(b1, o1);
+}
+
+// One wave a token.  The lanes are shared out to the groups, P = 2^lp for each, and
+// a group's experts to its lanes in turn: lane holds slots i = 0 .. NV - 1, expert
+// (lane / P) S + lane % P + P i of S a group.  (No groups: P = 64, S = E.)  So a
+// group's best two meet in the row of lanes that hold it, and dropping a group is
+// a lane's own business.
+//
+// The k-th best is found k times, by the high halves of the scores' keys: one
+// maximum over the wave in 32 bits.  Where more than one expert has that high half
+// (20 bits of the fraction), the low halves decide, then the experts' numbers.
 template <int ELEM, int NV, bool SIGMOID, bool GROUPED>
 __global__ void __launch_bounds__(kThreads)
-k_route_topk(RouteArgs a, int32_t* __restrict__ ids, float* __restrict__ weights) {
-  __shared__ double lds[GROUPED ? kThreads / 64 : 1][GROUPED ? NV * 64 : 1];
+k_route_topk(RouteArgs a, int lp, int32_t* __restrict__ ids, float* __restrict__ weights) {
+  __shared__ double picked[kThreads / 64][kRouteMaxTopK];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wave;
   if (t >= a.T) return;
-  const int E = a.E;
+  const int E = a.E, G = GROUPED ? a.n_group : 1, S = GROUPED ? E / G : E, P = GROUPED ? 1 << lp : 64;
+  const int grp = GROUPED ? lane >> lp : 0, sub = GROUPED ? lane & (P - 1) : lane;
+  const int first = grp * S + sub;  // this lane's first expert
   float l[NV];
+  double s[NV], c[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const bool here = sub + P * i < S && (!GROUPED || grp < G);
+    l[i] = here ? load_as_f32<ELEM>(a.logits, t * E + first + P * i) : -INFINITY;
+    c[i] = a.bias && here ? (double)a.bias[first + P * i] : 0.0;
+  }
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = e < E ? clean_logit(load_as_f32<ELEM>(a.logits, t * E + e)) : -INFINITY;
+    l[i] = clean_logit(l[i]);
     top = __builtin_fmaxf(top, l[i]);
   }
-  double s[NV];
-  double total = 0.0, inv = 1.0;
-  if constexpr (!SIGMOID) {
+  double inv = 1.0;
+  if constexpr (SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] = sigmoid_f64(l[i]);
+  } else {
     top = wave_max_f32(top);
+    double total = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      s[i] = l[i] > -INFINITY ? exp((double)l[i] - (double)top) : 0.0;
+      s[i] = l[i] > -INFINITY ? exp_f64((double)l[i] - (double)top) : 0.0;
       total += s[i];
     }
     total = wave_sum_f64(total);
     inv = total > 0.0 ? 1.0 / total : 0.0;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
   }
   u64 key[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane + 64 * i;
-    double c = s[i] * inv;
-    if (a.bias && e < E) c += (double)a.bias[e];
-    if (!(l[i] > -INFINITY) || !(c > -INFINITY)) c = -INFINITY;
-    key[i] = c > -INFINITY ? order_key(c) : 0;
-    if constexpr (GROUPED) lds[wave][e] = c;
+    if constexpr (!SIGMOID) s[i] *= inv;
+    c[i] += s[i];
+    if (!(l[i] > -INFINITY) || !(c[i] > -INFINITY)) c[i] = -INFINITY;
+    key[i] = c[i] > -INFINITY ? order_key(c[i]) : 0;
   }
   if constexpr (GROUPED) {
-    // P lanes share a group: each finds the best two of every P-th expert, then
-    // the lanes' are merged.  P = 64 / (n_group rounded up to a power of two).
-    wave_lds_fence();
-    const int G = a.n_group, S = E / G;
-    int lg = 0;
-    while ((1 << lg) < G) ++lg;
-    const int P = 64 >> lg, grp = lane / P;
     double b1 = -INFINITY, b2 = -INFINITY;
-    if (grp < G)
-      for (int j = lane % P; j < S; j += P) {
-        const double c = lds[wave][grp * S + j];
-        if (c > b1) { b2 = b1; b1 = c; }
-        else if (c > b2) b2 = c;
-      }
-    for (int d = 1; d < P; d <<= 1) {
-      const double o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
-      const double lo = b1 > o1 ? o1 : b1;
-      b1 = b1 > o1 ? b1 : o1;
-      const double hi2 = b2 > o2 ? b2 : o2;
-      b2 = lo > hi2 ? lo : hi2;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      b2 = __builtin_fmax(b2, __builtin_fmin(b1, c[i]));
+      b1 = __builtin_fmax(b1, c[i]);
+    }
+    if (lp > 0) merge_top2<kSwap1>(b1, b2);
+    if (lp > 1) merge_top2<kSwap2>(b1, b2);
+    if (lp > 2) merge_top2<kMirror8>(b1, b2);
+    if (lp > 3) merge_top2<kMirror16>(b1, b2);
+    if (lp > 4) {  // two groups
+      const double o1 = __shfl_xor(b1, 16), o2 = __shfl_xor(b2, 16);
+      b2 = __builtin_fmax(__builtin_fmin(b1, o1), __builtin_fmax(b2, o2));
+      b1 = __builtin_fmax(b1, o1);
     }
     if (a.group_top == 2 && b2 > -INFINITY) b1 += b2;
     // a group is kept if fewer than topk_group groups come before it
     int before = 0;
     for (int g = 0; g < G; ++g) {
-      const double o = __shfl(b1, g * P);
-      before += (o > b1) || (o == b1 && g < grp);
+      const double o = read_f64(b1, g << lp);
+      before += (int)(o > b1) + (int)(o == b1 && g < grp);
     }
-    u64 kept = 0;
-    const u64 mine = __ballot(grp < G && before < a.topk_group);
-    for (int g = 0; g < G; ++g) kept |= ((mine >> (g * P)) & 1ull) << g;
+    if (before >= a.topk_group) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 64 * i;
-      if (e < E && !((kept >> (e / S)) & 1ull)) key[i] = 0;
+      for (int i = 0; i < NV; ++i) key[i] = 0;
     }
   }
-  // top_k times the largest key; equal keys go to the lowest expert
   int id = -1;
   for (int j = 0; j < a.top_k; ++j) {
-    u64 best = 0;
-    int slot = 0;
+    uint32_t hi = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (key[i] > best) { best = key[i]; slot = i; }
-    const uint32_t hi = (uint32_t)(best >> 32), top_hi = wave_umax(hi);
-    if (top_hi == 0) break;  // no candidate is left (every score's key has a high half above 0)
-    u64 who = __ballot(hi == top_hi);
-    if (who & (who - 1)) {
-      const uint32_t lo = hi == top_hi ? (uint32_t)best : 0u, top_lo = wave_umax(lo);
-      who = __ballot(hi == top_hi && lo == top_lo);
-      if (who & (who - 1)) {
-        const uint32_t e = (who >> lane) & 1ull ? 0xFFFFu - (uint32_t)(lane + 64 * slot) : 0u;
-        const uint32_t first = wave_umax(e);
-        who = __ballot(e == first);
-      }
+    for (int i = 0; i < NV; ++i) hi = max(hi, (uint32_t)(key[i] >> 32));
+    const uint32_t most = wave_umax(hi);
+    if (most == 0) break;  // no candidate is left
+    u64 who[NV];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      who[i] = __ballot((uint32_t)(key[i] >> 32) == most);
+      n += __builtin_popcountll(who[i]);
     }
-    const int win = __builtin_ctzll(who);
-    const int e = win + 64 * __builtin_amdgcn_readlane(slot, win);
-    if (lane == j) id = e;
+    if (n > 1) {
+      uint32_t lo = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((uint32_t)(key[i] >> 32) == most) lo = max(lo, (uint32_t)key[i]);
+      lo = wave_umax(lo);
+      uint32_t e = 0;  // 65535 - the lowest expert
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (key[i] == ((u64)most << 32 | lo)) e = max(e, 65535u - (uint32_t)(first + P * i));
+      e = 65535u - wave_umax(e);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        who[i] = __ballot(key[i] == ((u64)most << 32 | lo) && (uint32_t)(first + P * i) == e);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (lane == win && slot == i) key[i] = 0;
+      if (who[i]) {
+        const int win = __builtin_ctzll(who[i]);
+        const int e = __builtin_amdgcn_readlane(first, win) + P * i;
+        if (lane == j) id = e;
+        if (lane == win) {
+          key[i] = 0;
+          picked[wave][j] = s[i];
+        }
+      }
   }
   // lane j: the weight of the j-th chosen
-  double w = 0.0;
-  const float lj = id >= 0 ? clean_logit(load_as_f32<ELEM>(a.logits, t * E + id)) : -INFINITY;
-  if constexpr (SIGMOID) {
-    if (id >= 0) w = 1.0 / (1.0 + exp(-(double)lj));
-    if (a.renormalize) {
-      const double sum = wave_sum_f64(w);
-      w = sum > 0.0 ? w / sum : 0.0;
+  wave_lds_fence();
+  double w = id >= 0 ? picked[wave][lane & (kRouteMaxTopK - 1)] : 0.0;
+  if (a.renormalize) {
+    if constexpr (!SIGMOID) {
+      // the softmax over the chosen ones, which holds also where the others dwarf them
+      const float lj = id >= 0 ? clean_logit(load_as_f32<ELEM>(a.logits, t * E + id)) : -INFINITY;
+      const float m = wave_max_f32(lj);
+      if (id >= 0) w = exp_f64((double)lj - (double)m);
     }
-  } else if (a.renormalize) {
-    // the softmax over the chosen ones
-    const float m = wave_max_f32(lj);
-    if (id >= 0) w = exp((double)lj - (double)m);
-    const double sum = wave_sum_f64(w);
+    const double sum = read_f64(sum16_f64(w), 0);  // the first 16 lanes
     w = sum > 0.0 ? w / sum : 0.0;
-  } else if (id >= 0) {
-    w = exp((double)lj - (double)top) * inv;
   }
   if (lane < a.top_k) {
     ids[t * a.top_k + lane] = id;
@@ -217,88 +307,105 @@ k_route_topk(RouteArgs a, int32_t* __restrict__ ids, float* __restrict__ weights
 //            unchosen have no gradient
 // One wave a token; a row is put together in LDS.  Lanes below top_k hold the
 // chosen; an id outside [0, E) takes no part.
-template <int ELEM, bool SIGMOID, bool DENSE>
+// NV: the dense form holds expert lane + 64 i in slot i.
+template <int ELEM, bool SIGMOID, bool DENSE, int NV>
 __global__ void __launch_bounds__(kThreads)
 k_route_topk_backward(RouteArgs a, const int32_t* __restrict__ ids, const float* __restrict__ dw,
                       void* __restrict__ d_logits) {
-  __shared__ float lds[kThreads / 64][kRouteMaxExperts];
+  __shared__ __align__(16) float lds[kThreads / 64][kRouteMaxExperts];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wave;
   if (t >= a.T) return;
   const int E = a.E;
   float* line = lds[wave];
-  for (int e = lane; e < E; e += 64) line[e] = 0.f;
+  for (int e = lane * 4; e < E; e += 256) *reinterpret_cast<float4*>(line + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+  float x[NV];
+  if constexpr (DENSE) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      x[i] = lane + 64 * i < E ? load_as_f32<ELEM>(a.logits, t * E + lane + 64 * i) : -INFINITY;
+  }
   int id = -1;
   double g = 0.0;
   float l = -INFINITY;
   if (lane < a.top_k) {
     id = ids[t * a.top_k + lane];
+    const float w = dw[t * a.top_k + lane];
     if ((unsigned)id >= (unsigned)E) id = -1;
     if (id >= 0) {
-      g = (double)dw[t * a.top_k + lane] * (double)a.scale;
+      g = (double)w * (double)a.scale;
       l = clean_logit(load_as_f32<ELEM>(a.logits, t * E + id));
     }
   }
+  // sums over the chosen: the first 16 lanes hold them
+  auto sum_of = [](double v) { return read_f64(sum16_f64(v), 0); };
   double d = 0.0;  // this lane's term
-  float top = -INFINITY, inv = 0.f;
+  float top = -INFINITY;
+  double inv = 0.0, mean = 0.0, s[NV];
   if constexpr (SIGMOID) {
-    const double z = exp(-(double)l), s = id >= 0 ? 1.0 / (1.0 + z) : 0.0;
-    const double rest = id >= 0 ? 1.0 / (1.0 + exp((double)l)) : 0.0;  // 1 - s
+    const double v = id >= 0 ? sigmoid_f64(l) : 0.0;
+    const double rest = id >= 0 ? sigmoid_f64(-l) : 0.0;  // 1 - s
     if (a.renormalize) {
-      const double sum = wave_sum_f64(s);
-      const double p = sum > 0.0 ? s / sum : 0.0;
-      d = p * rest * (g - wave_sum_f64(p * g));
+      const double sum = sum_of(v);
+      const double p = sum > 0.0 ? v / sum : 0.0;
+      d = p * rest * (g - sum_of(p * g));
     } else {
-      d = s * rest * g;
+      d = v * rest * g;
     }
   } else if constexpr (!DENSE) {
     const float m = wave_max_f32(l);
-    const double x = l > -INFINITY ? exp((double)l - (double)m) : 0.0;
-    const double sum = wave_sum_f64(x);
+    const double x = l > -INFINITY ? exp_f64((double)l - (double)m) : 0.0;
+    const double sum = sum_of(x);
     const double p = sum > 0.0 ? x / sum : 0.0;
-    d = p * (g - wave_sum_f64(p * g));
+    d = p * (g - sum_of(p * g));
   } else {
     double sum = 0.0;
-    for (int e = lane; e < E; e += 64)
-      top = __builtin_fmaxf(top, clean_logit(load_as_f32<ELEM>(a.logits, t * E + e)));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i] = clean_logit(x[i]);
+      top = __builtin_fmaxf(top, x[i]);
+    }
     top = wave_max_f32(top);
-    for (int e = lane; e < E; e += 64) {
-      const float v = clean_logit(load_as_f32<ELEM>(a.logits, t * E + e));
-      if (v > -INFINITY) sum += exp((double)v - (double)top);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      s[i] = x[i] > -INFINITY ? exp_f64((double)x[i] - (double)top) : 0.0;
+      sum += s[i];
     }
     sum = wave_sum_f64(sum);
-    const double s = l > -INFINITY ? exp((double)l - (double)top) / sum : 0.0;
+    inv = sum > 0.0 ? 1.0 / sum : 0.0;
+    const double p = l > -INFINITY ? exp_f64((double)l - (double)top) * inv : 0.0;
     d = g;
-    const double mean = wave_sum_f64(g * s);
-    inv = sum > 0.0 ? (float)(1.0 / sum) : 0.f;
-    g = mean;
+    mean = sum_of(g * p);
   }
   // an id that occurs more than once gets its terms' sum, in their order
   double mine = 0.0;
   for (int j = 0; j < a.top_k; ++j) {
-    const int ij = __shfl(id, j);
-    const double dj = __shfl(d, j);
+    const int ij = __builtin_amdgcn_readlane(id, j);
+    const double dj = read_f64(d, j);
     if (id == ij) mine += dj;
   }
   wave_lds_fence();
   if (id >= 0) line[id] = (float)mine;
   wave_lds_fence();
-  for (int e = lane; e < E; e += 64) {
-    float v = line[e];
-    if constexpr (DENSE) {
-      const float x = clean_logit(load_as_f32<ELEM>(a.logits, t * E + e));
-      v = x > -INFINITY ? (float)(exp((double)x - (double)top) * (double)inv * ((double)v - g)) : 0.f;
+  if constexpr (DENSE) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + 64 * i;
+      if (e < E) store_f32<ELEM>(d_logits, t * E + e, (float)(s[i] * inv * ((double)line[e] - mean)));
     }
-    store_f32<ELEM>(d_logits, t * E + e, v);
+  } else if ((E & 3) == 0) {
+    for (int e = lane * 4; e < E; e += 256) store4_f32<ELEM>(d_logits, t * E + e, *reinterpret_cast<const float4*>(line + e));
+  } else {
+    for (int e = lane; e < E; e += 64) store_f32<ELEM>(d_logits, t * E + e, line[e]);
   }
 }
 
 template <int ELEM, int NV>
-void route(const RouteArgs& a, int32_t* ids, float* w, hipStream_t stream) {
+void route(const RouteArgs& a, int lp, int32_t* ids, float* w, hipStream_t stream) {
   const dim3 grid((unsigned)((a.T + kThreads / 64 - 1) / (kThreads / 64)));
-  const bool sig = a.scoring == SCORE_SIGMOID, grouped = a.topk_group < a.n_group;
+  const bool sig = a.scoring == SCORE_SIGMOID, grouped = lp < 6;
   auto go = [&](auto SIG, auto GRP) {
-    hipLaunchKernelGGL((k_route_topk<ELEM, NV, SIG(), GRP()>), grid, dim3(kThreads), 0, stream, a, ids, w);
+    hipLaunchKernelGGL((k_route_topk<ELEM, NV, SIG(), GRP()>), grid, dim3(kThreads), 0, stream, a, lp, ids, w);
   };
   if (sig && grouped) go(std::true_type{}, std::true_type{});
   else if (sig) go(std::true_type{}, std::false_type{});
@@ -317,12 +424,18 @@ void by_elem(int elem, F f) {
 
 hipError_t launch_route_topk(const RouteArgs& a, int32_t* ids, float* weights, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
+  // lanes of a group, 2^lp; groups that are all kept are none
+  int lp = 6;
+  if (a.topk_group < a.n_group)
+    while ((64 >> lp) < a.n_group) --lp;
+  const int S = lp < 6 ? a.E / a.n_group : a.E, slots = (S + (1 << lp) - 1) >> lp;
   by_elem(a.elem, [&](auto ELEM) {
-    if (a.E <= 128) route<ELEM(), 2>(a, ids, weights, stream);
-    else if (a.E <= 256) route<ELEM(), 4>(a, ids, weights, stream);
-    else if (a.E <= 320) route<ELEM(), 5>(a, ids, weights, stream);
-    else if (a.E <= 512) route<ELEM(), 8>(a, ids, weights, stream);
-    else route<ELEM(), 16>(a, ids, weights, stream);
+    if (slots <= 2) route<ELEM(), 2>(a, lp, ids, weights, stream);
+    else if (slots <= 4) route<ELEM(), 4>(a, lp, ids, weights, stream);
+    else if (slots <= 5) route<ELEM(), 5>(a, lp, ids, weights, stream);
+    else if (slots <= 8) route<ELEM(), 8>(a, lp, ids, weights, stream);
+    else if (slots <= 16) route<ELEM(), 16>(a, lp, ids, weights, stream);
+    else route<ELEM(), 32>(a, lp, ids, weights, stream);
   });
   return hipGetLastError();
 }
@@ -332,13 +445,16 @@ hipError_t launch_route_topk_backward(const RouteArgs& a, const int32_t* ids, co
   if (a.T == 0) return hipSuccess;
   const dim3 grid((unsigned)((a.T + kThreads / 64 - 1) / (kThreads / 64)));
   by_elem(a.elem, [&](auto ELEM) {
-    auto go = [&](auto SIG, auto DENSE) {
-      hipLaunchKernelGGL((k_route_topk_backward<ELEM(), SIG(), DENSE()>), grid, dim3(kThreads), 0,
+    auto go = [&](auto SIG, auto DENSE, auto NV) {
+      hipLaunchKernelGGL((k_route_topk_backward<ELEM(), SIG(), DENSE(), NV()>), grid, dim3(kThreads), 0,
                          stream, a, ids, d_weights, d_logits);
     };
-    if (a.scoring == SCORE_SIGMOID) go(std::true_type{}, std::false_type{});
-    else if (a.renormalize) go(std::false_type{}, std::false_type{});
-    else go(std::false_type{}, std::true_type{});
+    typedef std::integral_constant<int, 1> none;
+    if (a.scoring == SCORE_SIGMOID) go(std::true_type{}, std::false_type{}, none{});
+    else if (a.renormalize) go(std::false_type{}, std::false_type{}, none{});
+    else if (a.E <= 256) go(std::false_type{}, std::true_type{}, std::integral_constant<int, 4>{});
+    else if (a.E <= 512) go(std::false_type{}, std::true_type{}, std::integral_constant<int, 8>{});
+    else go(std::false_type{}, std::true_type{}, std::integral_constant<int, 16>{});
   });
   return hipGetLastError();
 }
