@@ -29,6 +29,7 @@ moe_workspace_layout, moe_ring_layout, moe_select_split and moe_select_block_m.
 """
 
 import ctypes
+import importlib
 import os
 
 import torch
@@ -155,8 +156,25 @@ def lib():
     for name in EXPORTED_SYMBOLS:
         if name != "moe_last_error":
             getattr(L, name).restype = ctypes.c_int
+    _short_way(L)
     _lib = L
     return L
+
+
+# Module _fast (csrc/binding.cpp): functions that look a plain call's tensors over, make the C call
+# and return True; None where anything is not plain, which the functions below then do or refuse.
+_fast = None
+
+
+def _short_way(L):
+    global _fast
+    if _fast is None:
+        if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_fast.so")):
+            raise RuntimeError(
+                "_fast.so is missing beside the library: build both with "
+                "`python -m mixture_experts_ffn_moe_amd.build`")
+        _fast = importlib.import_module("._fast", __name__)
+    _fast.init(L._handle, torch._C._cuda_getCurrentRawStream)
 
 
 class MoeTune(ctypes.Structure):
@@ -877,6 +895,10 @@ def moe_route_topk(logits, top_k, bias=None, scoring="softmax", n_group=1, topk_
     preallocated.  moe_route_topk_backward is its gradient: with gradients
     enabled the call refuses logits that require one (make it inside a
     torch.autograd.Function)."""
+    if out is not None and stream is None and lib() and _fast.route_topk(
+            logits, bias, out[0], out[1], top_k, _SCORING.get(scoring), n_group, topk_group, group_top,
+            renormalize, scale):
+        return out[0], out[1]
     T, E, elem, code = _route_options(logits, scoring)
     dev = logits.device
     lp = _operand(logits, "logits", logits.dtype, (T, E), dev)
@@ -895,6 +917,9 @@ def moe_route_topk_backward(logits, topk_ids, d_weights, scoring="softmax", reno
     """Gradient of moe_route_topk's weights with respect to its logits, (T, E)
     of their type, from the same logits and options, topk_ids as it returned
     them and the weights' gradient (T, top_k) fp32."""
+    if out is not None and stream is None and lib() and _fast.route_topk_backward(
+            logits, topk_ids, d_weights, _SCORING.get(scoring), renormalize, scale, out):
+        return out
     T, E, elem, code = _route_options(logits, scoring)
     dev = logits.device
     _, k = _matrix(topk_ids, "topk_ids")
@@ -936,6 +961,9 @@ def moe_fp8_quant(x, scale_type="f32", rows=True, columns=False, num_tokens_post
     device count) rows behind it, and groups of 128 that begin behind it, are
     left as they are (unspecified in new tensors).  ``out`` may pass the four
     preallocated."""
+    if out is not None and stream is None and lib() and _fast.fp8_quant(
+            x, _SCALE.get(scale_type, (None,))[0], rows, columns, num_tokens_post_padded, *out):
+        return (*(out[:2] if rows else (None, None)), *(out[2:] if columns else (None, None)))
     M, K = _matrix(x, "x")
     dev = x.device
     elem = _float_elem(x, "x")
@@ -963,6 +991,9 @@ def moe_fp8_quant_weights(w, scale_type="f32", transposed=False, stream=None, ou
     ``transposed``: qt (E, K, N) and qt_scale, the weights with which moe_fp8_linear
     computes the gradient of its input; else None.  K, and N if transposed, are
     multiples of 16.  Scales as moe_fp8_quant's."""
+    if out is not None and stream is None and lib() and _fast.fp8_quant_weights(
+            w, _SCALE.get(scale_type, (None,))[0], transposed, *out):
+        return (*out[:2], *(out[2:] if transposed else (None, None)))
     if len(w.shape) != 3:
         raise MoeError(-2, f"w must have shape (E, N, K) (got {tuple(w.shape)})")
     E, N, K = w.shape
@@ -1012,6 +1043,9 @@ def moe_fp8_linear(x, x_scale, w, w_scale, expert_ids=None, num_tokens_post_padd
     tensor).  The gradient of x is this call on d_out quantized along its rows
     and the transposed weights (moe_fp8_quant_weights), the weights' is
     moe_fp8_linear_dw."""
+    if out is not None and stream is None and lib() and _fast.fp8_linear(
+            x, x_scale, w, w_scale, expert_ids, num_tokens_post_padded, block_m, out):
+        return out
     M, K = _matrix(x, "x")
     dev = x.device
     if len(w.shape) != 3:
@@ -1058,6 +1092,9 @@ def moe_fp8_linear_dw(dyt, dyt_scale, xt, xt_scale, num_experts=1, expert_ids=No
     fp32 or both uint8 e8m0.  Without ``expert_ids`` one layer; with a plan's
     (blocks of 128 or 256 rows, padding rows zeros) each expert's own rows, zeros
     for an expert without any."""
+    if out is not None and stream is None and lib() and _fast.fp8_linear_dw(
+            dyt, dyt_scale, xt, xt_scale, num_experts, expert_ids, num_tokens_post_padded, block_m, out):
+        return out
     N, M = _matrix(dyt, "dyt")
     K, _ = _matrix(xt, "xt")
     dev = dyt.device

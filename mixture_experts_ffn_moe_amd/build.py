@@ -2,8 +2,9 @@
 
     python -m mixture_experts_ffn_moe_amd.build [--jobs N]
 
-Every source under ``csrc/`` is compiled with hipcc for gfx950 and linked
-into one shared library next to this file.  The host-side parts of hipcc
+Every HIP source under ``csrc/`` is compiled with hipcc for gfx950 and linked
+into one shared library next to this file; ``binding.cpp``, the short way into
+it from Python, is compiled with g++ against torch's headers into ``_fast.so``.  The host-side parts of hipcc
 warn that they do not know the "packed-fp32-ops" target feature; that is
 expected (the flag only concerns device code).
 """
@@ -12,12 +13,14 @@ import argparse
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
+FAST = os.path.join(HERE, "_fast.so")
 SOURCES = ["abi.hip", "abi_fp8.hip", "abi_route.hip", "abi_rows.hip", "abi_w4.hip", "align.hip",
            "fp8_linear.hip", "moe_kernels.hip", "moe_tiled.hip", "probe.hip", "quant.hip",
            "route.hip", "rows.hip", "w4.hip"]
@@ -41,10 +44,30 @@ def _compile(src):
     return obj
 
 
+def _compile_binding():
+    import torch
+    from torch.utils import cpp_extension
+
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = FAST + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(x for p in includes for x in ("-isystem", p)),
+           os.path.join(CSRC, "binding.cpp"), "-L" + libs, "-lc10", "-ltorch_cpu", "-ltorch_python",
+           "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{' '.join(cmd)}\n{r.stderr}")
+    os.replace(tmp, FAST)
+
+
 def build(jobs=4, verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
