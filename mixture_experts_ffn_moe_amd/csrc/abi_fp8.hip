@@ -46,7 +46,7 @@ int moe_fp8_quant(int32_t elem, int32_t scale_type, const void* x, int64_t M, in
   if (rc) return rc;
   if ((rc = check_size("M", M, 0))) return rc;
   if ((rc = check_size("K", K, 16, 16))) return rc;
-  if (qt ? up(M, 128) > kMaxY || up(M, 128) * up(K, 128) * 256 > kMaxThreads : M * up(K, 128) > kMaxThreads)
+  if (qt ? up(M, 128) > kMaxY || up(M, 128) * up(K, 128) * 256 > kMaxThreads : M * up(K, 128) > kMaxThreads / 16)
     return abi_fail(MOE_ERR_UNSUPPORTED, "M * K is too large for one launch");
   if (!q && !qt && M > 0) return abi_fail(MOE_ERR_NULL, "neither q nor qt is given");
   if ((rc = check_ntp(num_tokens_post_padded, false))) return rc;

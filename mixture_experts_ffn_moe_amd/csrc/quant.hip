@@ -113,29 +113,27 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
 }
 
-// Rows: 16 lanes a group of 128, eight values each.  A thread has kUnroll groups
+// Rows: 16 lanes a group of 128, eight values each.  A thread has U groups
 // requested before it uses the first.
-constexpr int kUnroll = 4;
 constexpr int kGroups = kThreads / 16;  // groups of one pass of a workgroup
 
-template <int ELEM, int SCALE>
+template <int ELEM, int SCALE, int U>
 __global__ void __launch_bounds__(kThreads)
-k_quant_rows(QuantArgs a, int64_t G, int64_t total) {
+k_quant_rows(QuantArgs a, uint32_t G, uint32_t total) {
   const int sub = threadIdx.x & 15;
-  Eight<ELEM> v[kUnroll];
-  int64_t row[kUnroll], grp[kUnroll];
-  const int64_t M = a.ntp ? min((int64_t)max(*a.ntp, 0), a.M) : a.M;
-  const int64_t first = (int64_t)blockIdx.x * (kGroups * kUnroll) + (threadIdx.x >> 4);
+  Eight<ELEM> v[U];
+  uint32_t row[U], k[U];
+  const uint32_t M = (uint32_t)(a.ntp ? min((int64_t)max(*a.ntp, 0), a.M) : a.M), K = (uint32_t)a.K;
+  const uint32_t first = blockIdx.x * (kGroups * U) + (threadIdx.x >> 4);
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = first + u * kGroups;
-    row[u] = i < total ? i / G : a.M;
-    grp[u] = i - row[u] * G;
-    const int64_t k = grp[u] * 128 + sub * 8;
-    v[u] = row[u] < M && k < a.K ? load8<ELEM>(a.x, row[u] * a.K + k) : zero8<ELEM>();
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = first + u * kGroups;
+    row[u] = i < total ? i / G : M;
+    k[u] = (i - row[u] * G) * 128 + sub * 8;
+    v[u] = row[u] < M && k[u] < K ? load8<ELEM>(a.x, (int64_t)row[u] * K + k[u]) : zero8<ELEM>();
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = umax(m, abs_bits(value<ELEM>(v[u], j)));
@@ -145,12 +143,11 @@ k_quant_rows(QuantArgs a, int64_t G, int64_t total) {
     float f[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = value<ELEM>(v[u], j) * inv;
-    const int64_t k = grp[u] * 128 + sub * 8;
     if (row[u] < M) {
-      if (k < a.K)
-        *reinterpret_cast<uint2*>(a.q + row[u] * a.K + k) =
+      if (k[u] < K)
+        *reinterpret_cast<uint2*>(a.q + (int64_t)row[u] * K + k[u]) =
             make_uint2(pack4(f[0], f[1], f[2], f[3]), pack4(f[4], f[5], f[6], f[7]));
-      if (sub == 0) store_scale<SCALE>(a.qs, row[u] * G + grp[u], held);
+      if (sub == 0) store_scale<SCALE>(a.qs, first + u * kGroups, held);
     }
   }
 }
@@ -160,13 +157,27 @@ k_quant_rows(QuantArgs a, int64_t G, int64_t total) {
 // that whole 128-byte lines of a column are written.
 // BLOCK: one scale for the tile (weights; blockIdx.z the expert), q and, with COLS,
 // its transpose.  Else ROWS and COLS with scales of their own.
-constexpr int kPitch = 144;  // bytes of a column in LDS
+//
+// In LDS a column is 128 bytes and every access 8 or 16.  A wave writes 8 bytes of 16
+// columns 8 apart; so that these fall on all banks, chunk q of column 8 c + j lies at
+// chunk q ^ (c % 8) of column 8 c + (j ^ (c / 8)).
+__device__ __forceinline__ int turned(int c, int j, int byte) {
+  return ((8 * c + (j ^ (c >> 3))) << 7) + (byte ^ ((c & 7) << 4));
+}
+
+// Largest over the wave's lanes l % 16: both halves, both rows of each half.
+__device__ __forceinline__ uint32_t umax_rows(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = umax(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return umax(b[0], b[1]);
+}
 
 template <int ELEM, int SCALE, bool ROWS, bool COLS, bool BLOCK>
 __global__ void __launch_bounds__(kThreads)
 k_quant_tile(QuantArgs a, int64_t Mp, int64_t KB) {
-  __shared__ __align__(16) uint8_t turn[COLS ? 128 * kPitch : 16];
-  __shared__ uint32_t part[16][BLOCK ? 1 : 128];
+  __shared__ __align__(16) uint8_t turn[COLS ? 128 * 128 : 16];
+  __shared__ __align__(16) uint32_t part[4][BLOCK ? 4 : 128];
   const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
   const int64_t m0 = (int64_t)blockIdx.y * 128, k0 = (int64_t)blockIdx.x * 128;
   const int64_t M = a.ntp ? min((int64_t)max(*a.ntp, 0), a.M) : a.M;
@@ -187,10 +198,10 @@ k_quant_tile(QuantArgs a, int64_t Mp, int64_t KB) {
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) m = umax(m, abs_bits(value<ELEM>(v[i], j)));
-    m = umax16(m);
-    if (c == 0) part[r][0] = m;
+    m = umax_rows(umax16(m));
+    if ((threadIdx.x & 63) == 0) part[0][threadIdx.x >> 6] = m;
     __syncthreads();
-    m = umax16(part[c][0]);
+    m = umax(umax(part[0][0], part[0][1]), umax(part[0][2], part[0][3]));
     inv_block = group_scale<SCALE>(m, held);
     if (threadIdx.x == 0) {
       const int64_t NB = (a.M + 127) / 128;
@@ -224,20 +235,32 @@ k_quant_tile(QuantArgs a, int64_t Mp, int64_t KB) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) inv[j] = inv_block;
     } else {
+      uint32_t x[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        uint32_t x = 0;
+        x[j] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x = umax(x, abs_bits(value<ELEM>(v[i], j)));
-        part[r][8 * c + j] = x;
+        for (int i = 0; i < 8; ++i) x[j] = umax(x[j], abs_bits(value<ELEM>(v[i], j)));
+        x[j] = umax_rows(x[j]);
+      }
+      if ((threadIdx.x & 63) < 16) {
+        uint4* to = reinterpret_cast<uint4*>(&part[threadIdx.x >> 6][8 * c]);
+        to[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        to[1] = make_uint4(x[4], x[5], x[6], x[7]);
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t x = 0;
+      for (int j = 0; j < 8; ++j) x[j] = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x = umax(x, part[i][8 * c + j]);
-        inv[j] = group_scale<SCALE>(x, held);
+      for (int i = 0; i < 4; ++i) {
+        const uint4* from = reinterpret_cast<const uint4*>(&part[i][8 * c]);
+        const uint4 p = from[0], q = from[1];
+        x[0] = umax(x[0], p.x), x[1] = umax(x[1], p.y), x[2] = umax(x[2], p.z), x[3] = umax(x[3], p.w);
+        x[4] = umax(x[4], q.x), x[5] = umax(x[5], q.y), x[6] = umax(x[6], q.z), x[7] = umax(x[7], q.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        inv[j] = group_scale<SCALE>(x[j], held);
         if (r == 0 && k + j < a.K) store_scale<SCALE>(a.qts, (k + j) * (Mp / 128) + blockIdx.y, held);
       }
     }
@@ -246,7 +269,7 @@ k_quant_tile(QuantArgs a, int64_t Mp, int64_t KB) {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = value<ELEM>(v[i], j) * inv[j];
-      *reinterpret_cast<uint2*>(turn + (8 * c + j) * kPitch + 8 * r) =
+      *reinterpret_cast<uint2*>(turn + turned(c, j, 8 * r)) =
           make_uint2(pack4(f[0], f[1], f[2], f[3]), pack4(f[4], f[5], f[6], f[7]));
     }
     __syncthreads();
@@ -257,7 +280,7 @@ k_quant_tile(QuantArgs a, int64_t Mp, int64_t KB) {
       const int col = (threadIdx.x >> 3) + 32 * u, at = (threadIdx.x & 7) * 16;
       if (k0 + col < a.K && m0 + at < end)
         *reinterpret_cast<uint4*>(a.qt + z * a.M * a.K * (BLOCK ? 1 : 0) + (k0 + col) * end + m0 + at) =
-            *reinterpret_cast<const uint4*>(turn + col * kPitch + at);
+            *reinterpret_cast<const uint4*>(turn + turned(col >> 3, col & 7, at));
     }
   }
 }
@@ -280,9 +303,16 @@ hipError_t launch_quant(const QuantArgs& a, hipStream_t stream) {
   const int64_t G = (a.K + 127) / 128, Mp = (a.M + 127) / 128 * 128;
   by_types(a.elem, a.scale_type, [&](auto ELEM, auto SCALE) {
     if (!a.qt) {
-      const int64_t total = a.M * G, per = kGroups * kUnroll;
-      hipLaunchKernelGGL((k_quant_rows<ELEM(), SCALE()>), dim3((unsigned)((total + per - 1) / per)),
-                         dim3(kThreads), 0, stream, a, G, total);
+      // one group a thread where the call is small, four where there are many
+      // workgroups: more requests in flight (8192 x 4096 bf16: see below)
+      const int64_t total = a.M * G;
+      auto go = [&](auto U) {
+        constexpr int64_t per = kGroups * U();
+        hipLaunchKernelGGL((k_quant_rows<ELEM(), SCALE(), U()>), dim3((unsigned)((total + per - 1) / per)),
+                           dim3(kThreads), 0, stream, a, (uint32_t)G, (uint32_t)total);
+      };
+      if (total <= 2048 * kGroups) go(std::integral_constant<int, 1>{});
+      else go(std::integral_constant<int, 4>{});
       return;
     }
     const dim3 grid((unsigned)G, (unsigned)(Mp / 128));
