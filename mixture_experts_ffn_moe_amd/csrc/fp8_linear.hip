@@ -245,6 +245,8 @@ __device__ __forceinline__ int join_blocks(const Fp8Args& a, int nb, int per, in
   return tiles;
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 // Where a tile's operands lie, all wave-uniform.
 struct Source {
   const uint8_t* x;   // first row of X, first step
@@ -501,50 +503,55 @@ struct Tiles {
     return p.rows == BM && p.n0 + BN <= a.N && (a.N & 7) == 0;
   }
 
-  // Rounds and writes the sums: a lane has row m, n to n + 7 and n + 32 to n + 39.
-  // The stores go past the caches: what reads the output next is another kernel,
-  // and it must not push the operands out (8192 x 7168 x 4096 in e8m0: 200 us
-  // through the caches, 187 past them).
+  // Eight values at row `row` of the tile, columns n .. n + 7, as far as they exist.
+  __device__ __forceinline__ void store8(const At& p, int row, int64_t n, const u32x4& v) const {
+    if (row >= p.rows || n >= a.N) return;
+    uint16_t* o = static_cast<uint16_t*>(a.out) + (p.out + row) * a.N + n;
+    if ((a.N & 7) == 0) {
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(o));
+    } else if (n + 8 <= a.N) {
+      typedef u32x4 u32x4_any __attribute__((aligned(2)));  // rows of any length: at the element's alignment
+      *reinterpret_cast<u32x4_any*>(o) = v;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (n + c < a.N) o[c] = (uint16_t)(v[c / 2] >> (16 * (c & 1)));
+    }
+  }
+
+  // Rounds and writes the sums.  A lane has row m, n to n + 7 and n + 32 to n + 39 of
+  // them; lanes r and r + 8 trade halves and the lanes change places, so that a store
+  // writes eight rows of 128 bytes (32 experts' weights' gradients, 537 MB: 255 us
+  // with 64 bytes of 16 rows, 200 so).  The stores go past the caches: what reads the
+  // output next is another kernel, and it must not push the operands out (8192 x
+  // 7168 x 4096 in e8m0: 200 us through the caches, 187 past them).
   __device__ __forceinline__ void store(const At& p, const f32x4 (&acc)[MI][NI]) const {
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    const int64_t n = p.n0 + wn * 64 + g * 8;
-    const bool lines = whole(p);
+    const bool lines = whole(p), low = r16 < 8;
+    const int from = ((lane & 3) * 16 + (lane >> 3) + 8 * ((lane >> 2) & 1)) * 4;
+    const int row = wm * TM + (lane >> 3);
+    const int64_t n = p.n0 + wn * 64 + 8 * (lane & 7);
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
-      u32x4 v[2];
+      u32x4 v[2], first, second;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           v[h][c] = pack2<OELEM>(acc[mi][2 * h + c / 2][2 * (c & 1)], acc[mi][2 * h + c / 2][2 * (c & 1) + 1]);
-      if (lines) {
-        // lanes r and r + 8 trade halves and the lanes change places, so that a store
-        // writes eight rows of 128 bytes (32 experts' weights' gradients, 537 MB:
-        // 255 us with 64 bytes of 16 rows, 200 so)
-        const bool low = r16 < 8;
-        const int from = ((lane & 3) * 16 + (lane >> 3) + 8 * ((lane >> 2) & 1)) * 4;
-        u32x4 first, second;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t give = low ? v[1][c] : v[0][c];
-          const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0x128, 0xF, 0xF, true);  // row_ror 8
-          first[c] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(low ? v[0][c] : got));
-          second[c] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(low ? got : v[1][c]));
-        }
-        uint16_t* o = static_cast<uint16_t*>(a.out) + (p.out + wm * TM + 16 * mi + (lane >> 3)) * a.N + p.n0 +
-                      wn * 64 + 8 * (lane & 7);
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t give = low ? v[1][c] : v[0][c];
+        const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0x128, 0xF, 0xF, true);  // row_ror 8
+        first[c] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(low ? v[0][c] : got));
+        second[c] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(low ? got : v[1][c]));
+      }
+      if (lines) {
+        uint16_t* o = static_cast<uint16_t*>(a.out) + (p.out + row + 16 * mi) * a.N + n;
         __builtin_nontemporal_store(first, reinterpret_cast<u32x4*>(o));
         __builtin_nontemporal_store(second, reinterpret_cast<u32x4*>(o + 8 * a.N));
       } else {
-        const int m = wm * TM + 16 * mi + r16;
-        uint16_t* o = static_cast<uint16_t*>(a.out) + (p.out + m) * a.N + n;
-        if (m < p.rows) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              if (n + 32 * h + c < a.N) o[32 * h + c] = (uint16_t)(c & 1 ? v[h][c / 2] >> 16 : v[h][c / 2]);
-        }
+        store8(p, row + 16 * mi, n, first);
+        store8(p, row + 16 * mi + 8, n, second);
       }
     }
   }
@@ -783,7 +790,10 @@ hipError_t launch_fp8_linear(const Fp8Args& a, hipStream_t stream) {
     if (a.dw) {
       if (a.experts) tiles<O, S, true, true>(a, stream);
       else tiles<O, S, true, false>(a, stream);
-    } else if (rows <= 16) {
+    } else if (rows <= 16 || (!a.experts && up(a.M, 16) * up(a.N, 16) <= cus())) {
+      // also where 16 x 16 pieces do not outnumber the CUs: a tile's LDS and its
+      // groups' sums cost more than reading X and W once more (100 rows of 4096 by 512:
+      // 6.6 us, tiles 10.0; by 1024, 448 pieces: 11.2 and 10.0)
       few_rows<O, S, 1>(a, stream);
     } else if (rows <= 32) {
       few_rows<O, S, 2>(a, stream);
