@@ -118,6 +118,44 @@ def test_scores_nearer_than_fp32():
     assert ids.tolist() == [[50, 40, 0]]
 
 
+def test_near_the_border_in_32_bits():
+    # scores, and groups' sums, closer than 32-bit scores can tell, in every direction; the other tokens are ordinary
+    g = torch.Generator().manual_seed(3)
+    T, E, k = 64, 96, 5
+    l = torch.randn(T, E, generator=g)
+    bias = torch.randn(E, generator=g).mul(0.1)
+    for t in range(0, T, 2):
+        a, b = 7 + t % 3, 50 + t
+        b %= E
+        s = torch.sigmoid(l[t].double()) + bias.double()
+        # expert b's logit so that its score lies (t - T / 2) 2^-25 from the k-th best's
+        kth = torch.sort(s, descending=True)[0][k - 1 - t % 2]
+        want = (kth + (t - T // 2) * 2.0 ** -25 - bias[b].double()).clamp(1e-6, 1 - 1e-6)
+        l[t, b] = torch.log(want / (1 - want)).float()
+    for groups, kept, top in ((1, 1, 1), (6, 2, 2), (6, 2, 1), (3, 1, 2)):
+        check(l, k, bias, scoring="sigmoid", n_group=groups, topk_group=kept, group_top=top)
+    # two groups whose sums differ in the 60th bit, or not at all
+    l = torch.zeros(4, 64)
+    bias = torch.zeros(64)
+    bias[1], bias[33], bias[34] = 2.0 ** -30, 2.0 ** -31, 2.0 ** -31
+    l[1, 40] = 1e-7
+    l[2, 3] = -1e-7
+    check(l, 3, bias, scoring="sigmoid", n_group=2, topk_group=1, group_top=2)
+    check(l, 3, bias * 1e6, scoring="sigmoid", n_group=2, topk_group=1, group_top=2)
+    check(l + 60.0, 3, bias, scoring="sigmoid", n_group=4, topk_group=2, group_top=2)
+    check(l - 90.0, 3, bias, scoring="sigmoid", n_group=4, topk_group=2, group_top=2)
+
+
+def test_large_biases():
+    l = logits_of(40, 128, "f32", 5)
+    g = torch.Generator().manual_seed(6)
+    for size in (1e3, 1e6, 1e20, 3e38):
+        bias = torch.randn(128, generator=g).mul(size).clamp(-3.3e38, 3.3e38)
+        check(l, 8, bias, scoring="sigmoid", n_group=8, topk_group=3, group_top=1)
+        if size < 1e30:
+            check(l, 8, bias, scoring="sigmoid", n_group=8, topk_group=3, group_top=2)
+
+
 def test_many_tokens():
     l = logits_of(2051, 288, "f32", 9)
     ids, w = moe.moe_route_topk(l.cuda(), 8, scoring="sigmoid", n_group=8, topk_group=4, group_top=2)
