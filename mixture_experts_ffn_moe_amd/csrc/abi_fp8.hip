@@ -91,7 +91,9 @@ int moe_fp8_linear(int32_t elem, int32_t scale_type, const void* x, const void* 
   if (expert_ids && block_m != 16 && block_m != 32 && block_m != 64 && block_m != 128 && block_m != 256)
     return abi_fail(MOE_ERR_UNSUPPORTED, "block_m must be 16, 32, 64, 128 or 256 (got %d)", block_m);
   const bool few = (expert_ids ? block_m : M) <= 32;  // a workgroup for each 16 rows of weights
-  if (few ? up(M, 16) * 512 > kMaxThreads / up(N, 16) : up(M, 64) > kMaxSize / up(N, 64))
+  const bool blocks64 = expert_ids && block_m == 64;   // one for each block and 128 of them
+  if (few ? up(M, 16) * 512 > kMaxThreads / up(N, 16)
+          : up(M, 64) > (blocks64 ? kMaxThreads / 512 : kMaxSize) / up(N, 64))
     return abi_fail(MOE_ERR_UNSUPPORTED, "M * N is too large for one launch");
   if ((rc = check_ntp(num_tokens_post_padded, expert_ids != nullptr))) return rc;
   if ((rc = check_ptrs({{x, M > 0}, {x_scale, M > 0}, {w, M > 0}, {w_scale, M > 0}, {expert_ids, false},

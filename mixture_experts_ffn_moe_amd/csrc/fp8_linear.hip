@@ -176,7 +176,7 @@ k_fp8_rows(Fp8Args a) {
 // CU that stays and takes tile after tile; a tile's last step requests the next
 // one's first, which arrives while the sums are written.  k_fp8_tile (smaller tiles
 // where those would leave CUs idle): a workgroup a tile, KG groups of waves that
-// take the steps in turn and add up in the end, more stages ahead.
+// take the steps in turn, each with two stages, and add up in the end.
 constexpr int kRow = 128;
 constexpr int kMaxPlanExperts = kFp8MaxPlanExperts;
 constexpr int kMaxPlanBlocks = 2048;  // of a layer over a plan whose blocks are put together
@@ -263,22 +263,21 @@ struct At {
   int rows, e;
 };
 
-template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int NS, int KG>
+template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int KG>
 struct Tiles {
   static constexpr int MI = TM / 16, NI = 4;
   static constexpr int WN = BN / 64, WM = BM / TM, NW = WM * WN;  // waves of a group
   static constexpr int X = BM * kRow, W = BN * kRow;
   static constexpr int S = NW * 256;  // scales: 64 rows a wave, X's then W's
-  static constexpr int STAGE = X + W + S, LDS = NS * STAGE;
+  static constexpr int STAGE = X + W + S, LDS = 2 * KG * STAGE;  // two stages a group
   static constexpr int XI = X / 1024 / NW, WI = W / 1024 / NW;  // 16-byte loads a wave and stage
-  static constexpr int LOADS = XI + WI + 1;                     // with the scales
   static constexpr int LROWS = NW * 8;                          // rows of one 16-byte load
   static constexpr int PER = (XI + WI + MI - 1) / MI;           // loads beside a row subtile's products
   static constexpr int THREADS = NW * KG * 64;
   static constexpr int TAB = !PLAN ? 1 : DW ? 2 * kMaxPlanExperts : BM > 128 ? kMaxPlanBlocks + 1 : 1;
   static constexpr int SB = SCALE == SCALE_F32 ? 4 : 1;
   static_assert(X % (1024 * NW) == 0 && W % (1024 * NW) == 0 && (BM + BN) / 64 <= NW && BM % 64 == 0);
-  static_assert(NS % KG == 0 && LDS <= 160 * 1024 && (KG == 1 || (KG - 1) * NW * MI * NI * 1024 <= LDS));
+  static_assert(LDS <= 160 * 1024 && (KG == 1 || (KG - 1) * NW * MI * NI * 1024 <= LDS));
 
   const Fp8Args& a;
   uint8_t* smem;
@@ -322,7 +321,7 @@ struct Tiles {
         count[e] = 0;
       }
       __syncthreads();
-      const int nb = min(max(*a.ntp, 0) / a.block_m, a.n_blocks);
+      const int nb = min((int)min((int64_t)max(*a.ntp, 0), a.K) / a.block_m, a.n_blocks);  // a.K: the rows there are
       for (int b = threadIdx.x; b < nb; b += THREADS) {
         const int e = a.experts[b];
         if ((unsigned)e < (unsigned)a.E) {
@@ -564,7 +563,7 @@ __device__ __forceinline__ void zero(T& acc) {
 }
 
 template <int OELEM, int SCALE, bool DW, bool PLAN>
-using Stay = Tiles<OELEM, SCALE, DW, PLAN, 256, 256, 128, 2, 1>;
+using Stay = Tiles<OELEM, SCALE, DW, PLAN, 256, 256, 128, 1>;
 
 template <int OELEM, int SCALE, bool DW, bool PLAN>
 __global__ void __launch_bounds__((Stay<OELEM, SCALE, DW, PLAN>::THREADS))
@@ -625,11 +624,10 @@ k_fp8_stay(Fp8Args a, int mtiles, int ntiles) {
   wait_vmcnt<0>();  // the last step's requests write LDS too
 }
 
-template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int NS, int KG>
-__global__ void __launch_bounds__((Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, NS, KG>::THREADS))
+template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int KG>
+__global__ void __launch_bounds__((Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG>::THREADS))
 k_fp8_tile(Fp8Args a, int mtiles, int ntiles) {
-  using C = Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, NS, KG>;
-  constexpr int D = NS / KG;  // stages of a group
+  using C = Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
   __shared__ int tab[C::TAB];
   const C c(a, smem, tab, mtiles, ntiles);
@@ -648,15 +646,12 @@ k_fp8_tile(Fp8Args a, int mtiles, int ntiles) {
     return f;
   };
   const int rounds = (src.steps + KG - 1) / KG;
-#pragma unroll
-  for (int i = 0; i < D - 1; ++i) c.load(source(i), i * KG + kg, i * KG + kg);
-  int slot = 0;
+  c.load(source(0), kg, kg);
   for (int i = 0; i < rounds; ++i) {
-    wait_vmcnt<C::LOADS * (D - 2)>();
+    wait_vmcnt<0>();
     lds_barrier();
-    const int ahead = i + D - 1, to = slot == 0 ? D - 1 : slot - 1;
-    c.add(slot * KG + kg, acc, source(ahead), ahead * KG + kg, to * KG + kg);
-    slot = slot + 1 == D ? 0 : slot + 1;
+    const int slot = (i & 1) * KG + kg, other = KG - (i & 1) * KG + kg;
+    c.add(slot, acc, source(i + 1), (i + 1) * KG + kg, other);
   }
   wait_vmcnt<0>();  // the last requests write LDS too
   if constexpr (KG > 1) {
@@ -724,11 +719,11 @@ void stay_kernel(const Fp8Args& a, hipStream_t stream) {
   else go(std::false_type{});
 }
 
-template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int NS, int KG>
+template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int KG>
 void tile_kernel(const Fp8Args& a, hipStream_t stream) {
   const int64_t mt = row_tiles<DW>(a, BM), nt = up(a.N, BN), tiles = mt * nt * (DW ? a.E : 1);
-  hipLaunchKernelGGL((k_fp8_tile<OELEM, SCALE, DW, PLAN, BM, BN, TM, NS, KG>), dim3((unsigned)(up(tiles, 8) * 8)),
-                     dim3(Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, NS, KG>::THREADS), 0, stream, a, (int)mt,
+  hipLaunchKernelGGL((k_fp8_tile<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG>), dim3((unsigned)(up(tiles, 8) * 8)),
+                     dim3(Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG>::THREADS), 0, stream, a, (int)mt,
                      (int)nt);
 }
 
@@ -767,15 +762,15 @@ void tiles(const Fp8Args& a, hipStream_t stream) {
   // a plan's block of rows lies in one tile
   const int least = PLAN && !DW ? a.block_m : 64;
   if (least <= 64) {
-    if (count(64) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 64, 16, 8, 4>(a, stream);
-    if (count(64) <= 2 * n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 64, 16, 4, 2>(a, stream);
+    if (count(64) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 64, 16, 4>(a, stream);
+    if (count(64) <= 2 * n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 64, 16, 2>(a, stream);
     // blocks of 64 rows: the weights' bytes are the time (512 tokens, 64 experts,
     // top-6, 4096 x 4096: 217 us; 64 x 64 tiles 262)
-    if constexpr (PLAN && !DW) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 128, 32, 2, 1>(a, stream);
+    if constexpr (PLAN && !DW) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 128, 32, 1>(a, stream);
   }
   if (least <= 128) {
-    if (count(128) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 64, 4, 2>(a, stream);
-    if (count(128) <= 2 * n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 64, 2, 1>(a, stream);
+    if (count(128) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 64, 2>(a, stream);
+    if (count(128) <= 2 * n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 64, 1>(a, stream);
   }
   stay_kernel<OELEM, SCALE, DW>(a, stream);
 }

@@ -57,6 +57,7 @@ def test_outputs_are_16_bits():
     (linear, dict(M=-1), SHAPE), (linear, dict(K=8), SHAPE), (linear, dict(N=0), SHAPE), (linear, dict(E=0), SHAPE),
     (linear, dict(E=2), SHAPE), (linear, dict(N=1 << 27), UNSUPPORTED), (linear, dict(M=1 << 26, N=1 << 19), UNSUPPORTED),
     (linear, dict(M=1 << 23, N=1 << 12, **{**PLAN, 'bm': 16}), UNSUPPORTED),
+    (linear, dict(M=1 << 24, N=1 << 12, **{**PLAN, 'bm': 64}), UNSUPPORTED),
     (linear, {**PLAN, "bm": 48}, UNSUPPORTED), (linear, {**PLAN, "bm": 0}, UNSUPPORTED), (linear, {**PLAN, "ntp": None}, NULL),
     (linear, {**PLAN, "ntp": P((1 << 20) + 2)}, ALIGN),
     (linear, dict(K=(1 << 22) + 16), UNSUPPORTED), (dw, dict(M=(1 << 22) + 128), UNSUPPORTED),

@@ -220,6 +220,32 @@ def test_scales_of_nothing_and_nan():
     assert torch.equal(out[keep], clean[keep])
 
 
+@pytest.mark.parametrize("ntp", [-3, 0, 100, 128, 300, 384, 1000, 1 << 30])
+def test_row_counts_that_fit_nothing(ntp):
+    # a count counts as at most the buffers' rows, at least none; a dw's whole blocks below it
+    rng = np.random.default_rng(9)
+    M, K, N, E, bm = 384, 144, 72, 3, 128
+    x, w = operand((M, K), (M, 2), "f32", rng, True), operand((E * N, K), (E, 2), "f32", rng, True)
+    w = w[0].reshape(E, N, K), w[1].reshape(E, 1, 2)
+    ids = np.array([0, 2, 2, 1, 1], np.int32)  # more than there are rows for
+    experts, count = torch.from_numpy(ids).cuda(), torch.tensor([ntp], dtype=torch.int32, device="cuda")
+    n = max(0, min(ntp, M))
+    out = torch.full((M, N), MARK, dtype=torch.bfloat16, device="cuda")
+    moe.moe_fp8_linear(*gpu(x), *gpu(w), experts, count, bm, out=out)
+    for b in range(3):
+        at = slice(b * bm, min((b + 1) * bm, n))
+        if at.start < n:
+            close(out[at], fp8.row_values(*x)[at], fp8.block_values(w[0][ids[b]], w[1][ids[b]]), "bf16", True)
+    assert (out[n:] == MARK).all()
+    dy, xt = operand((N, M), (N, 3), "f32", rng, True), operand((K, M), (K, 3), "f32", rng, True)
+    g = moe.moe_fp8_linear_dw(*gpu(dy), *gpu(xt), E, experts, count, bm)
+    of = np.full(M, -1)
+    of[:n // bm * bm] = ids[:3].repeat(bm)[:n // bm * bm]
+    for e in range(E):
+        close(g[e], fp8.row_values(*dy)[:, of == e], fp8.row_values(*xt)[:, of == e], "bf16", True) if (of == e).any() else None
+        assert (of == e).any() or not g[e].any()
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_same_bits_and_graph(M, kind):
