@@ -176,7 +176,7 @@ k_fp8_rows(Fp8Args a) {
 // CU that stays and takes tile after tile; a tile's last step requests the next
 // one's first, which arrives while the sums are written.  k_fp8_tile (smaller tiles
 // where those would leave CUs idle): a workgroup a tile, KG groups of waves that
-// take the steps in turn, each with two stages, and add up in the end.
+// take the steps in turn, each with D stages, and add up in the end.
 constexpr int kRow = 128;
 constexpr int kMaxPlanExperts = kFp8MaxPlanExperts;
 constexpr int kMaxPlanBlocks = 2048;  // of a layer over a plan whose blocks are put together
@@ -263,14 +263,15 @@ struct At {
   int rows, e;
 };
 
-template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int KG>
+template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int KG, int D>
 struct Tiles {
   static constexpr int MI = TM / 16, NI = 4;
   static constexpr int WN = BN / 64, WM = BM / TM, NW = WM * WN;  // waves of a group
   static constexpr int X = BM * kRow, W = BN * kRow;
   static constexpr int S = NW * 256;  // scales: 64 rows a wave, X's then W's
-  static constexpr int STAGE = X + W + S, LDS = 2 * KG * STAGE;  // two stages a group
+  static constexpr int STAGE = X + W + S, LDS = D * KG * STAGE;  // D stages a group
   static constexpr int XI = X / 1024 / NW, WI = W / 1024 / NW;  // 16-byte loads a wave and stage
+  static constexpr int LOADS = XI + WI + 1;                     // with the scales
   static constexpr int LROWS = NW * 8;                          // rows of one 16-byte load
   static constexpr int PER = (XI + WI + MI - 1) / MI;           // loads beside a row subtile's products
   static constexpr int THREADS = NW * KG * 64;
@@ -563,7 +564,7 @@ __device__ __forceinline__ void zero(T& acc) {
 }
 
 template <int OELEM, int SCALE, bool DW, bool PLAN>
-using Stay = Tiles<OELEM, SCALE, DW, PLAN, 256, 256, 128, 1>;
+using Stay = Tiles<OELEM, SCALE, DW, PLAN, 256, 256, 128, 1, 2>;
 
 template <int OELEM, int SCALE, bool DW, bool PLAN>
 __global__ void __launch_bounds__((Stay<OELEM, SCALE, DW, PLAN>::THREADS))
@@ -624,10 +625,10 @@ k_fp8_stay(Fp8Args a, int mtiles, int ntiles) {
   wait_vmcnt<0>();  // the last step's requests write LDS too
 }
 
-template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int KG>
-__global__ void __launch_bounds__((Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG>::THREADS))
+template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int KG, int D>
+__global__ void __launch_bounds__((Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG, D>::THREADS))
 k_fp8_tile(Fp8Args a, int mtiles, int ntiles) {
-  using C = Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG>;
+  using C = Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG, D>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
   __shared__ int tab[C::TAB];
   const C c(a, smem, tab, mtiles, ntiles);
@@ -646,12 +647,15 @@ k_fp8_tile(Fp8Args a, int mtiles, int ntiles) {
     return f;
   };
   const int rounds = (src.steps + KG - 1) / KG;
-  c.load(source(0), kg, kg);
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) c.load(source(i), i * KG + kg, i * KG + kg);
+  int slot = 0;
   for (int i = 0; i < rounds; ++i) {
-    wait_vmcnt<0>();
+    wait_vmcnt<C::LOADS * (D - 2)>();
     lds_barrier();
-    const int slot = (i & 1) * KG + kg, other = KG - (i & 1) * KG + kg;
-    c.add(slot, acc, source(i + 1), (i + 1) * KG + kg, other);
+    const int ahead = i + D - 1, to = slot == 0 ? D - 1 : slot - 1;
+    c.add(slot * KG + kg, acc, source(ahead), ahead * KG + kg, to * KG + kg);
+    slot = slot + 1 == D ? 0 : slot + 1;
   }
   wait_vmcnt<0>();  // the last requests write LDS too
   if constexpr (KG > 1) {
@@ -719,11 +723,11 @@ void stay_kernel(const Fp8Args& a, hipStream_t stream) {
   else go(std::false_type{});
 }
 
-template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int KG>
+template <int OELEM, int SCALE, bool DW, bool PLAN, int BM, int BN, int TM, int KG, int D>
 void tile_kernel(const Fp8Args& a, hipStream_t stream) {
   const int64_t mt = row_tiles<DW>(a, BM), nt = up(a.N, BN), tiles = mt * nt * (DW ? a.E : 1);
-  hipLaunchKernelGGL((k_fp8_tile<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG>), dim3((unsigned)(up(tiles, 8) * 8)),
-                     dim3(Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG>::THREADS), 0, stream, a, (int)mt,
+  hipLaunchKernelGGL((k_fp8_tile<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG, D>), dim3((unsigned)(up(tiles, 8) * 8)),
+                     dim3(Tiles<OELEM, SCALE, DW, PLAN, BM, BN, TM, KG, D>::THREADS), 0, stream, a, (int)mt,
                      (int)nt);
 }
 
@@ -750,27 +754,27 @@ void few_rows(const Fp8Args& a, hipStream_t stream) {
 // Tiles as large as still fill the CUs: a step of a large tile takes longer, but
 // moves fewer bytes for its products.  K = 7168, N = 4096, fp32 scales, us for M =
 // 128 / 512 / 1024 / 2048 / 8192:
-//   64 x 64, four groups of waves       20 / 40 / 76 / 150 / 608  (one a CU)
-//   64 x 64, two groups                 24 / 29 / 55 / 108 / 430  (two a CU)
-//   128 x 128, two groups               35 / 35 / 37 / 73 / 296   (one a CU)
-//   128 x 128                           52 / 53 / 52 / 72 / 286   (two a CU)
-//   256 x 256, staying                  96 / 87 / 87 / 87 / 211   (one a CU)
+//   64 x 64, two groups of three stages      16 / 32 / 61 / 119 / 483
+//   64 x 128, two groups of three stages     21 / 23 / 45 / 88 / 354
+//   128 x 128, two groups of two stages      35 / 35 / 38 / 73 / 301
+//   128 x 128, one of two (two a CU)         47 / 48 / 49 / 70 / 283
+//   256 x 256, staying                       87 / 91 / 91 / 92 / 219
 template <int OELEM, int SCALE, bool DW, bool PLAN>
 void tiles(const Fp8Args& a, hipStream_t stream) {
   const int64_t n = cus(), E = DW ? a.E : 1;
-  auto count = [&](int B) { return row_tiles<DW>(a, B) * up(a.N, B) * E; };
+  auto count = [&](int BM, int BN) { return row_tiles<DW>(a, BM) * up(a.N, BN) * E; };
   // a plan's block of rows lies in one tile
   const int least = PLAN && !DW ? a.block_m : 64;
   if (least <= 64) {
-    if (count(64) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 64, 16, 4>(a, stream);
-    if (count(64) <= 2 * n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 64, 16, 2>(a, stream);
+    if (count(64, 64) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 64, 16, 2, 3>(a, stream);
+    if (count(64, 128) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 128, 32, 2, 3>(a, stream);
     // blocks of 64 rows: the weights' bytes are the time (512 tokens, 64 experts,
     // top-6, 4096 x 4096: 217 us; 64 x 64 tiles 262)
-    if constexpr (PLAN && !DW) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 128, 32, 1>(a, stream);
+    if constexpr (PLAN && !DW) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 128, 32, 1, 2>(a, stream);
   }
   if (least <= 128) {
-    if (count(128) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 64, 2>(a, stream);
-    if (count(128) <= 2 * n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 64, 1>(a, stream);
+    if (count(128, 128) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 64, 2, 2>(a, stream);
+    if (count(128, 128) <= 2 * n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 32, 1, 2>(a, stream);
   }
   stay_kernel<OELEM, SCALE, DW>(a, stream);
 }
