@@ -757,6 +757,8 @@ int moe_route_topk_backward(int32_t elem, const void* logits, const int32_t* top
  * Sums: MOE_SCALE_F32 adds each 128's sum in fp32; inside 128 (and for
  * MOE_SCALE_E8M0 throughout) the matrix instruction adds, whose sums keep about
  * 16 bits of the products' norm (moe_mfma_probe), so outputs are bf16 or fp16.
+ * A row's and a weight's fp32 scale are multiplied with each other first: their
+ * product must not overflow, and below 2^-126 it loses bits.
  * Every element of the output's rows in use is written.  The same inputs give
  * the same bits.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
  * MOE_ERR_ALIGN, MOE_ERR_HIP.
@@ -800,7 +802,8 @@ int moe_fp8_linear(int32_t elem, int32_t scale_type, const void* x, const void* 
  * expert_ids NULL: one layer (E = 1), all M rows.  Else the plan's n_blocks ids
  * for blocks of block_m = 128 or 256 rows, an expert's in one run, as the planner
  * lays them out (E <= 1024); an expert without rows gets zeros.  Padding rows must
- * be zeros (moe_permute writes them so).  M == 0 writes zeros. */
+ * be zeros (moe_permute writes them so), as must those behind num_tokens_post_padded
+ * inside its last 128 (moe_fp8_quant writes them so).  M == 0 writes zeros. */
 int moe_fp8_linear_dw(int32_t elem, int32_t scale_type, const void* dyt, const void* dyt_scale,
                       const void* xt, const void* xt_scale, const int32_t* expert_ids,
                       const int32_t* num_tokens_post_padded, void* dw, int64_t M, int64_t N, int64_t K,

@@ -1061,6 +1061,7 @@ def moe_fp8_linear(x, x_scale, w, w_scale, expert_ids=None, num_tokens_post_padd
     ids, ntp = _plan_blocks(expert_ids, num_tokens_post_padded, block_m, M, dev)
     elem, dtype = _out_elem(out, dtype)
     out = _output(out, "out", (M, N), dtype, dev, stream)
+    _outside_autograd(x, x_scale, w, w_scale)
     _enqueue(lib().moe_fp8_linear, dev, stream, elem, kind, xp, xs, wp, ws, ids, ntp, out.data_ptr(), M, K,
              N, E, block_m)
     return out
@@ -1111,6 +1112,7 @@ def moe_fp8_linear_dw(dyt, dyt_scale, xt, xt_scale, num_experts=1, expert_ids=No
     ids, ntp = _plan_blocks(expert_ids, num_tokens_post_padded, block_m, None, dev)
     elem, dtype = _out_elem(out, dtype)
     out = _output(out, "out", (num_experts, N, K), dtype, dev, stream)
+    _outside_autograd(dyt, dyt_scale, xt, xt_scale)
     _enqueue(lib().moe_fp8_linear_dw, dev, stream, elem, kind, dp, ds, xp, xs, ids, ntp, out.data_ptr(), M,
              N, K, num_experts, block_m, 0 if ids is None else expert_ids.numel())
     return out

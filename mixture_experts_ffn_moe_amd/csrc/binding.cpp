@@ -210,6 +210,7 @@ PyObject* fp8_linear(PyObject* const* a) {
   const at::Tensor* w = c.tensor(a[2]);
   const at::Tensor* out = c.tensor(a[7]);
   if (!c.plain || x->dim() != 2 || w->dim() != 3) return done(false);
+  for (int i = 0; i < 4; ++i) c.outside_autograd(c.tensor(a[i]));
   const int64_t M = x->size(0), K = x->size(1), E = w->size(0), N = w->size(1);
   const int code = scale_of(xs->scalar_type()), elem = elem_of(out->scalar_type());
   if (code < 0 || elem < 0 || elem > MOE_ELEM_F16) return done(false);
@@ -243,6 +244,7 @@ PyObject* fp8_linear_dw(PyObject* const* a) {
   const at::Tensor* x = c.tensor(a[2]);
   const at::Tensor* out = c.tensor(a[8]);
   if (!c.plain || dy->dim() != 2 || x->dim() != 2) return done(false);
+  for (int i = 0; i < 4; ++i) c.outside_autograd(c.tensor(a[i]));
   const int64_t N = dy->size(0), M = dy->size(1), K = x->size(0), E = c.integer(a[4], 1, kMost);
   const int code = scale_of(dys->scalar_type()), elem = elem_of(out->scalar_type());
   if (code < 0 || elem < 0 || elem > MOE_ELEM_F16 || M % 128) return done(false);

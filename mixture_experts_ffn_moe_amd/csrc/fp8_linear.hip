@@ -322,7 +322,7 @@ struct Tiles {
         count[e] = 0;
       }
       __syncthreads();
-      const int nb = min((int)min((int64_t)max(*a.ntp, 0), a.K) / a.block_m, a.n_blocks);  // a.K: the rows there are
+      const int nb = min((int)((summed() + a.block_m - 1) / a.block_m), a.n_blocks);
       for (int b = threadIdx.x; b < nb; b += THREADS) {
         const int e = a.experts[b];
         if ((unsigned)e < (unsigned)a.E) {
@@ -347,6 +347,9 @@ struct Tiles {
     lds0 = lds_addr(smem);
   }
 
+  // The rows in use that a plan's gradient sums over.
+  __device__ __forceinline__ int64_t summed() const { return min((int64_t)max(*a.ntp, 0), a.K); }
+
   // Tile t in the order of the walk: bands of four row tiles by all columns, so that
   // the tiles that run together on one XCD share both operands in its L2
   __device__ __forceinline__ At place(int t, Source& src) const {
@@ -364,7 +367,7 @@ struct Tiles {
     if constexpr (PLAN && DW) {
       const int count = __builtin_amdgcn_readfirstlane(tab[kMaxPlanExperts + z]);
       k0 = count ? (int64_t)__builtin_amdgcn_readfirstlane(tab[z]) * a.block_m : 0;
-      k1 = min(k0 + (int64_t)count * a.block_m, a.K);
+      k1 = min(k0 + (int64_t)count * a.block_m, summed());
     } else if constexpr (PLAN) {
       int first = mt, past = mt + 1;
       if (joined) {

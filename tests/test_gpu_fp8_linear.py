@@ -222,7 +222,7 @@ def test_scales_of_nothing_and_nan():
 
 @pytest.mark.parametrize("ntp", [-3, 0, 100, 128, 300, 384, 1000, 1 << 30])
 def test_row_counts_that_fit_nothing(ntp):
-    # a count counts as at most the buffers' rows, at least none; a dw's whole blocks below it
+    # a count counts as at most the buffers' rows, at least none; a dw's whole 128s that begin below it
     rng = np.random.default_rng(9)
     M, K, N, E, bm = 384, 144, 72, 3, 128
     x, w = operand((M, K), (M, 2), "f32", rng, True), operand((E * N, K), (E, 2), "f32", rng, True)
@@ -240,7 +240,7 @@ def test_row_counts_that_fit_nothing(ntp):
     dy, xt = operand((N, M), (N, 3), "f32", rng, True), operand((K, M), (K, 3), "f32", rng, True)
     g = moe.moe_fp8_linear_dw(*gpu(dy), *gpu(xt), E, experts, count, bm)
     of = np.full(M, -1)
-    of[:n // bm * bm] = ids[:3].repeat(bm)[:n // bm * bm]
+    of[:up(n) * 128] = ids[:3].repeat(bm)[:up(n) * 128]
     for e in range(E):
         close(g[e], fp8.row_values(*dy)[:, of == e], fp8.row_values(*xt)[:, of == e], "bf16", True) if (of == e).any() else None
         assert (of == e).any() or not g[e].any()
@@ -280,3 +280,36 @@ def test_same_bits_and_graph(M, kind):
     o = moe.moe_fp8_linear(*sets[0][0], *[v[None] for v in sets[0][1]], stream=s)
     s.synchronize()
     assert torch.equal(o, out)
+
+
+@pytest.mark.parametrize("ntp", [0, 128, 256, 384, 640, 1 << 30])
+def test_dw_rows_that_end_inside_a_block(ntp):
+    # blocks of 256 rows over buffers of 640: the last one's rows are those there are
+    rng = np.random.default_rng(ntp % 1000)
+    M, N, K, E, bm = 640, 72, 200, 3, 256
+    ids = np.array([2, 0, 0], np.int32)
+    dy, xt = operand((N, M), (N, 5), "f32", rng, True), operand((K, M), (K, 5), "f32", rng, True)
+    g = moe.moe_fp8_linear_dw(*gpu(dy), *gpu(xt), E, torch.from_numpy(ids).cuda(),
+                              torch.tensor([ntp], dtype=torch.int32, device="cuda"), bm)
+    of = ids.repeat(bm)[:M]
+    of[min(ntp, M):] = -1
+    for e in range(E):
+        close(g[e], fp8.row_values(*dy)[:, of == e], fp8.row_values(*xt)[:, of == e], "bf16", True)
+
+
+def test_refuses_a_gradient_that_would_be_lost():
+    rng = np.random.default_rng(1)
+    x, w = gpu(operand((8, 128), (8, 1), "f32", rng, True)), gpu(operand((16, 128), (1, 1), "f32", rng, True))
+    w = [v[None] for v in w]
+    out = torch.empty(8, 16, dtype=torch.bfloat16, device="cuda")
+    t = gpu(operand((16, 128), (16, 1), "f32", rng, True))
+    for o in (None, out):
+        for at in range(2):
+            s = [x[1], w[1]]
+            s[at] = s[at].clone().requires_grad_()
+            with pytest.raises(moe.MoeError, match="autograd"):
+                moe.moe_fp8_linear(x[0], s[0], w[0], s[1], out=o)
+            with torch.no_grad():
+                moe.moe_fp8_linear(x[0], s[0], w[0], s[1], out=o)
+    with pytest.raises(moe.MoeError, match="autograd"):
+        moe.moe_fp8_linear_dw(t[0], t[1].clone().requires_grad_(), *t)
