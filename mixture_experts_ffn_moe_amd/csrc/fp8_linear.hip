@@ -305,7 +305,8 @@ struct Tiles {
     joined = false;
     if constexpr (PLAN && !DW) {
       M = min((int64_t)max(*a.ntp, 0), a.M);
-      valid = (int)((M + a.block_m - 1) / a.block_m);
+      const int rows = min(a.block_m, BM);  // a block is a tile, or tiles of BM rows
+      valid = (int)((M + rows - 1) / rows);
       // Blocks that follow each other with one expert are put together into tiles of up
       // to BM rows: tab[t] is tile t's first block and, above, its expert.  More
       // blocks than fit are tiles of their own.
@@ -369,18 +370,19 @@ struct Tiles {
       k0 = count ? (int64_t)__builtin_amdgcn_readfirstlane(tab[z]) * a.block_m : 0;
       k1 = min(k0 + (int64_t)count * a.block_m, summed());
     } else if constexpr (PLAN) {
-      int first = mt, past = mt + 1;
       if (joined) {
         const int at = __builtin_amdgcn_readfirstlane(tab[mt]);
-        first = at & (2 * kMaxPlanBlocks - 1);
-        past = __builtin_amdgcn_readfirstlane(tab[mt + 1]) & (2 * kMaxPlanBlocks - 1);
+        const int past = __builtin_amdgcn_readfirstlane(tab[mt + 1]) & (2 * kMaxPlanBlocks - 1);
         p.e = at / (2 * kMaxPlanBlocks);
+        p.m0 = (int64_t)(at & (2 * kMaxPlanBlocks - 1)) * a.block_m;
+        end = min((int64_t)past * a.block_m, M);
       } else {
-        p.e = __builtin_amdgcn_readfirstlane(a.experts[mt]);
+        const int rows = min(a.block_m, BM);
+        p.e = __builtin_amdgcn_readfirstlane(a.experts[mt / (a.block_m / rows)]);
+        p.m0 = (int64_t)mt * rows;
+        end = min(p.m0 + rows, M);
       }
       if ((unsigned)p.e >= (unsigned)a.E) p.e = -1;
-      p.m0 = (int64_t)first * a.block_m;
-      end = min((int64_t)past * a.block_m, M);
     }
     p.rows = (int)max(min(end - p.m0, (int64_t)BM), (int64_t)0);
     p.out = (DW ? z * a.M : 0) + p.m0;
@@ -708,10 +710,22 @@ int cus() {
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to; }
 
-// row tiles of BM rows: of a plan at most as many as blocks
+// row tiles of BM rows; of a plan's smaller blocks at most as many as blocks
 template <bool DW>
 int64_t row_tiles(const Fp8Args& a, int BM) {
-  return up(a.M, a.experts && !DW ? a.block_m : BM);
+  return up(a.M, a.experts && !DW && a.block_m < BM ? a.block_m : BM);
+}
+
+// Rows of a plan that are likely in use.  Its buffers have room for a block that is
+// not whole with every expert; by shares of equal size, r, an expert has r rows and
+// those to its block's end, and at least half a block of them where shares differ.
+// (1506 tokens, 21 experts, top-3, blocks of 128, K = 2176, N = 1040: 22.6 us with the
+// tiles that this gives, 128 x 128; 29.6 with 256 x 256, which all rows would give.)
+int64_t rows_likely(const Fp8Args& a) {
+  const int64_t room = (int64_t)a.E * (a.block_m - 1);
+  if (a.M <= room + a.E) return a.M;
+  const int64_t whole = a.E * up((a.M - room) / a.E, a.block_m) * a.block_m;
+  return min(a.M, max(whole, a.M - room / 2));
 }
 
 template <int OELEM, int SCALE, bool DW>
@@ -765,20 +779,17 @@ void few_rows(const Fp8Args& a, hipStream_t stream) {
 template <int OELEM, int SCALE, bool DW, bool PLAN>
 void tiles(const Fp8Args& a, hipStream_t stream) {
   const int64_t n = cus(), E = DW ? a.E : 1;
-  auto count = [&](int BM, int BN) { return row_tiles<DW>(a, BM) * up(a.N, BN) * E; };
-  // a plan's block of rows lies in one tile
-  const int least = PLAN && !DW ? a.block_m : 64;
-  if (least <= 64) {
-    if (count(64, 64) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 64, 16, 2, 3>(a, stream);
-    if (count(64, 128) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 128, 32, 2, 3>(a, stream);
-    // blocks of 64 rows: the weights' bytes are the time (512 tokens, 64 experts,
-    // top-6, 4096 x 4096: 217 us; 64 x 64 tiles 262)
-    if constexpr (PLAN && !DW) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 128, 32, 1, 2>(a, stream);
-  }
-  if (least <= 128) {
-    if (count(128, 128) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 64, 2, 2>(a, stream);
-    if (count(128, 128) <= 2 * n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 32, 1, 2>(a, stream);
-  }
+  Fp8Args likely = a;
+  if constexpr (PLAN && !DW) likely.M = rows_likely(a);
+  auto count = [&](int BM, int BN) { return row_tiles<DW>(likely, BM) * up(a.N, BN) * E; };
+  if (count(64, 64) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 64, 16, 2, 3>(a, stream);
+  if (count(64, 128) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 128, 32, 2, 3>(a, stream);
+  // blocks of 64 rows: the weights' bytes are the time (512 tokens, 64 experts,
+  // top-6, 4096 x 4096: 217 us; 64 x 64 tiles 262)
+  if constexpr (PLAN && !DW)
+    if (a.block_m == 64) return tile_kernel<OELEM, SCALE, DW, PLAN, 64, 128, 32, 1, 2>(a, stream);
+  if (count(128, 128) <= n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 64, 2, 2>(a, stream);
+  if (count(128, 128) <= 2 * n) return tile_kernel<OELEM, SCALE, DW, PLAN, 128, 128, 32, 1, 2>(a, stream);
   stay_kernel<OELEM, SCALE, DW>(a, stream);
 }
 
