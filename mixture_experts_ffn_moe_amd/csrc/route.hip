@@ -165,6 +165,11 @@ __device__ __forceinline__ void merge_top2(double& b1, double& b2) {
 // The k-th best is found k times, by the high halves of the scores' keys: one
 // maximum over the wave in 32 bits.  Where more than one expert has that high half
 // (20 bits of the fraction), the low halves decide, then the experts' numbers.
+//
+// 8192 tokens, 288 experts in 8 groups, top-8, sigmoid: 14 us, of which the launch and
+// the loads are 5, the selection 4.7, the scores 2.3, the groups 1.1 and the weights 1:
+// vector instructions and chains of lane movements, not bytes (9.5 MB, 2 us).  8 tokens:
+// 5.1, one such chain.
 template <int ELEM, int NV, bool SIGMOID, bool GROUPED>
 __global__ void __launch_bounds__(kThreads)
 k_route_topk(RouteArgs a, int lp, int32_t* __restrict__ ids, float* __restrict__ weights) {
@@ -308,6 +313,8 @@ k_route_topk(RouteArgs a, int lp, int32_t* __restrict__ ids, float* __restrict__
 // One wave a token; a row is put together in LDS.  Lanes below top_k hold the
 // chosen; an id outside [0, E) takes no part.
 // NV: the dense form holds expert lane + 64 i in slot i.
+// 8192 tokens, 288 experts, fp32: 6.8 us, the launch and then the writes (9.4 MB; the
+// sparse forms read the chosen logits only, 5.6 MB of lines).
 template <int ELEM, bool SIGMOID, bool DENSE, int NV>
 __global__ void __launch_bounds__(kThreads)
 k_route_topk_backward(RouteArgs a, const int32_t* __restrict__ ids, const float* __restrict__ dw,
