@@ -313,3 +313,28 @@ def test_refuses_a_gradient_that_would_be_lost():
                 moe.moe_fp8_linear(x[0], s[0], w[0], s[1], out=o)
     with pytest.raises(moe.MoeError, match="autograd"):
         moe.moe_fp8_linear_dw(t[0], t[1].clone().requires_grad_(), *t)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bm", [128, 256])
+@pytest.mark.parametrize("N", [500, 1000, 2000, 4000, 5000])
+def test_blocks_of_several_tiles(N, bm, kind):
+    # 2048 rows in blocks: tiles of 64 x 64 up to 256 x 256 as N grows, one block elsewhere, the last one cut off
+    rng = np.random.default_rng(N + bm)
+    M, K, E = 2048, 144, 5
+    ids = rng.integers(0, E, M // bm).astype(np.int32)
+    ids[2] = -1
+    ntp = M - bm + 100
+    x, w = operand((M, K), (M, 2), kind, rng, True), operand((E * N, K), (E * up(N), 2), kind, rng, True)
+    w = w[0].reshape(E, N, K), w[1].reshape(E, up(N), 2)
+    out = torch.full((M, N), MARK, dtype=torch.bfloat16, device="cuda")
+    moe.moe_fp8_linear(*gpu(x), *gpu(w), torch.from_numpy(ids).cuda(),
+                       torch.tensor([ntp], dtype=torch.int32, device="cuda"), bm, out=out)
+    values = fp8.row_values(*x)
+    for b, e in enumerate(ids):
+        at = slice(b * bm, min((b + 1) * bm, ntp))
+        if e < 0:
+            assert not out[at].any()
+        else:
+            close(out[at], values[at], fp8.block_values(w[0][e], w[1][e]), "bf16", True)
+    assert (out[ntp:] == MARK).all()
