@@ -310,22 +310,29 @@ k_route_topk(RouteArgs a, int lp, int32_t* __restrict__ ids, float* __restrict__
 //   sigmoid  dl_e = g_e s_e (1 - s_e)          of the chosen e, else 0
 //   softmax  dl_e = s_e (g_e - sum_j g_j s_j); renormalised, the sum is 0 and the
 //            unchosen have no gradient
-// One wave a token; a row is put together in LDS.  Lanes below top_k hold the
-// chosen; an id outside [0, E) takes no part.
-// NV: the dense form holds expert lane + 64 i in slot i.
+// One wave a token.  Lanes below top_k hold the chosen; an id outside [0, E) takes no
+// part.  The sparse forms put a row together in LDS.  The dense form holds expert lane
+// + 64 i in slot i; LDS has a byte for each expert, which of the chosen it is, and their
+// terms in 64 bits: where one expert has nearly all of the softmax, its g and the sum
+// differ by little, and either of them rounded to fp32 first would be most of the
+// difference.  (A row of doubles in LDS instead: as fast to 512 experts, 27.3 us for
+// 23.3 at 1000.)
 // 8192 tokens, 288 experts, fp32: 6.8 us, the launch and then the writes (9.4 MB; the
-// sparse forms read the chosen logits only, 5.6 MB of lines).
+// sparse forms read the chosen logits only, 5.6 MB of lines); dense, 10.
 template <int ELEM, bool SIGMOID, bool DENSE, int NV>
 __global__ void __launch_bounds__(kThreads)
 k_route_topk_backward(RouteArgs a, const int32_t* __restrict__ ids, const float* __restrict__ dw,
                       void* __restrict__ d_logits) {
-  __shared__ __align__(16) float lds[kThreads / 64][kRouteMaxExperts];
+  using cell_t = std::conditional_t<DENSE, uint8_t, float>;
+  constexpr int PER = 4 / sizeof(cell_t) * 4;  // of 16 bytes
+  __shared__ __align__(16) cell_t lds[kThreads / 64][kRouteMaxExperts];
+  __shared__ double terms[DENSE ? kThreads / 64 : 1][kRouteMaxTopK + 1];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wave;
   if (t >= a.T) return;
   const int E = a.E;
-  float* line = lds[wave];
-  for (int e = lane * 4; e < E; e += 256) *reinterpret_cast<float4*>(line + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+  cell_t* line = lds[wave];
+  for (int e = lane * PER; e < E; e += 64 * PER) *reinterpret_cast<uint4*>(line + e) = make_uint4(0, 0, 0, 0);
   float x[NV];
   if constexpr (DENSE) {
 #pragma unroll
@@ -392,13 +399,18 @@ k_route_topk_backward(RouteArgs a, const int32_t* __restrict__ ids, const float*
     if (id == ij) mine += dj;
   }
   wave_lds_fence();
-  if (id >= 0) line[id] = (float)mine;
+  if constexpr (DENSE) {
+    if (id >= 0) line[id] = (uint8_t)(lane + 1);
+    if (lane <= kRouteMaxTopK) terms[wave][(lane + 1) % (kRouteMaxTopK + 1)] = lane < a.top_k ? mine : 0.0;
+  } else {
+    if (id >= 0) line[id] = (float)mine;
+  }
   wave_lds_fence();
   if constexpr (DENSE) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 64 * i;
-      if (e < E) store_f32<ELEM>(d_logits, t * E + e, (float)(s[i] * inv * ((double)line[e] - mean)));
+      if (e < E) store_f32<ELEM>(d_logits, t * E + e, (float)(s[i] * inv * (terms[wave][line[e]] - mean)));
     }
   } else if ((E & 3) == 0) {
     for (int e = lane * 4; e < E; e += 256) store4_f32<ELEM>(d_logits, t * E + e, *reinterpret_cast<const float4*>(line + e));
