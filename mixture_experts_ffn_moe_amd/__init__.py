@@ -162,7 +162,8 @@ def lib():
 
 
 # Module _fast (csrc/binding.cpp): functions that look a plain call's tensors over, make the C call
-# and return True; None where anything is not plain, which the functions below then do or refuse.
+# and return True (or raise, where the launch fails); None where anything is not plain, which the
+# functions below then do or refuse.
 _fast = None
 
 
@@ -174,7 +175,7 @@ def _short_way(L):
                 "_fast.so is missing beside the library: build both with "
                 "`python -m mixture_experts_ffn_moe_amd.build`")
         _fast = importlib.import_module("._fast", __name__)
-    _fast.init(L._handle, torch._C._cuda_getCurrentRawStream)
+    _fast.init(L._handle, torch._C._cuda_getCurrentRawStream, _check)
 
 
 class MoeTune(ctypes.Structure):

@@ -6,8 +6,10 @@
 // checks).  Each function here looks at the tensors directly, and where all is as
 // the call needs it (dense tensors of the right types and sizes on the current
 // device, outputs given) makes the C call on the current stream and returns True.
-// Anything else returns None and does nothing: the binding in Python then goes
-// its own way, which finds and words the error, or serves the less plain call.
+// Anything else enqueues nothing and returns None, also arguments that the C call
+// refuses: the binding in Python then goes its own way, which finds and words the
+// error, or serves the less plain call.  A launch that fails raises at once, since
+// the same call made again might succeed and hide it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <dlfcn.h>
@@ -29,6 +31,7 @@ decltype(&moe_fp8_linear) f_fp8_linear;
 decltype(&moe_fp8_linear_dw) f_fp8_linear_dw;
 int (*f_get_device)(int*);  // hipGetDevice
 PyObject* raw_stream;       // torch._C._cuda_getCurrentRawStream
+PyObject* launch_failed;    // called with MOE_ERR_HIP, raises
 
 // One call's arguments: whether all was plain so far, and the device.
 struct Call {
@@ -101,9 +104,18 @@ int scale_of(at::ScalarType t) { return t == at::kFloat ? MOE_SCALE_F32 : t == a
 at::ScalarType scale_type(int64_t code) { return code == MOE_SCALE_F32 ? at::kFloat : at::kByte; }
 int64_t groups(int64_t n) { return (n + 127) / 128; }
 
-PyObject* done(bool made) {
-  if (made) Py_RETURN_TRUE;
-  Py_RETURN_NONE;
+PyObject* not_plain() { Py_RETURN_NONE; }
+
+// The outcome of the C call.
+PyObject* made(int status) {
+  if (status == MOE_OK) Py_RETURN_TRUE;
+  if (status != MOE_ERR_HIP) Py_RETURN_NONE;  // refused before anything was enqueued
+  PyObject* code = launch_failed ? PyLong_FromLong(status) : nullptr;
+  PyObject* r = code ? PyObject_CallOneArg(launch_failed, code) : nullptr;
+  Py_XDECREF(code);
+  Py_XDECREF(r);
+  if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "a launch failed");
+  return nullptr;
 }
 
 // No C++ exception leaves a function of the module.
@@ -125,7 +137,7 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* route_topk(PyObject* const* a) {
   Call c;
   const at::Tensor* l = c.tensor(a[0]);
-  if (!l || l->dim() != 2) return done(false);
+  if (!l || l->dim() != 2) return not_plain();
   c.outside_autograd(l);
   const int64_t T = l->size(0), E = l->size(1), k = c.integer(a[4], 1, kMost);
   const int elem = elem_of(l->scalar_type());
@@ -136,10 +148,10 @@ PyObject* route_topk(PyObject* const* a) {
   const int64_t top = c.integer(a[8], 1, 2), renorm = c.integer(a[9], 0, 1);
   const double scale = c.real(a[10]);
   void* s = c.stream();
-  if (!c.plain || elem < 0 || E > kMost) return done(false);
-  return done(f_route_topk(elem, l->data_ptr(), static_cast<const float*>(bias), T, (int)E, (int)k, (int)scoring, (int)ng,
+  if (!c.plain || elem < 0 || E > kMost) return not_plain();
+  return made(f_route_topk(elem, l->data_ptr(), static_cast<const float*>(bias), T, (int)E, (int)k, (int)scoring, (int)ng,
                            (int)tg, (int)top, (int)renorm, (float)scale, static_cast<int32_t*>(ids),
-                           static_cast<float*>(w), s) == MOE_OK);
+                           static_cast<float*>(w), s));
 }
 
 // logits, ids, d_weights, scoring, renormalize, scale, d_logits
@@ -148,7 +160,7 @@ PyObject* route_topk_backward(PyObject* const* a) {
   const at::Tensor* l = c.tensor(a[0]);
   const at::Tensor* i = c.tensor(a[1]);
   const at::Tensor* d = c.tensor(a[2]);
-  if (!c.plain || l->dim() != 2 || i->dim() != 2) return done(false);
+  if (!c.plain || l->dim() != 2 || i->dim() != 2) return not_plain();
   c.outside_autograd(l);
   c.outside_autograd(d);
   const int64_t T = l->size(0), E = l->size(1), k = i->size(1);
@@ -159,16 +171,16 @@ PyObject* route_topk_backward(PyObject* const* a) {
   const double scale = c.real(a[5]);
   void* out = c.data(a[6], l->scalar_type(), {T, E});
   void* s = c.stream();
-  if (!c.plain || elem < 0 || E > kMost || k > kMost) return done(false);
-  return done(f_route_topk_backward(elem, l->data_ptr(), static_cast<const int32_t*>(ids), static_cast<const float*>(dw), T,
-                                    (int)E, (int)k, (int)scoring, (int)renorm, (float)scale, out, s) == MOE_OK);
+  if (!c.plain || elem < 0 || E > kMost || k > kMost) return not_plain();
+  return made(f_route_topk_backward(elem, l->data_ptr(), static_cast<const int32_t*>(ids), static_cast<const float*>(dw), T,
+                                    (int)E, (int)k, (int)scoring, (int)renorm, (float)scale, out, s));
 }
 
 // x, scale code, rows, columns, num_tokens_post_padded, q, q_scale, qt, qt_scale
 PyObject* fp8_quant(PyObject* const* a) {
   Call c;
   const at::Tensor* x = c.tensor(a[0]);
-  if (!x || x->dim() != 2) return done(false);
+  if (!x || x->dim() != 2) return not_plain();
   c.outside_autograd(x);
   const int64_t M = x->size(0), K = x->size(1), code = c.integer(a[1], 0, 1);
   const int elem = elem_of(x->scalar_type());
@@ -179,16 +191,15 @@ PyObject* fp8_quant(PyObject* const* a) {
   void* qt = columns ? c.data(a[7], at::kFloat8_e4m3fn, {K, 128 * groups(M)}) : nullptr;
   void* qts = columns ? c.data(a[8], scale_type(code), {K, groups(M)}) : nullptr;
   void* s = c.stream();
-  if (!c.plain || elem < 0 || !(rows || columns)) return done(false);
-  return done(f_fp8_quant(elem, (int)code, x->data_ptr(), M, K, static_cast<const int32_t*>(ntp), q, qs, qt, qts, s) ==
-              MOE_OK);
+  if (!c.plain || elem < 0 || !(rows || columns)) return not_plain();
+  return made(f_fp8_quant(elem, (int)code, x->data_ptr(), M, K, static_cast<const int32_t*>(ntp), q, qs, qt, qts, s));
 }
 
 // w, scale code, transposed, q, q_scale, qt, qt_scale
 PyObject* fp8_quant_weights(PyObject* const* a) {
   Call c;
   const at::Tensor* w = c.tensor(a[0]);
-  if (!w || w->dim() != 3) return done(false);
+  if (!w || w->dim() != 3) return not_plain();
   c.outside_autograd(w);
   const int64_t E = w->size(0), N = w->size(1), K = w->size(2), code = c.integer(a[1], 0, 1);
   const int elem = elem_of(w->scalar_type());
@@ -198,8 +209,8 @@ PyObject* fp8_quant_weights(PyObject* const* a) {
   void* qt = turned ? c.data(a[5], at::kFloat8_e4m3fn, {E, K, N}) : nullptr;
   void* qts = turned ? c.data(a[6], scale_type(code), {E, groups(K), groups(N)}) : nullptr;
   void* s = c.stream();
-  if (!c.plain || elem < 0) return done(false);
-  return done(f_fp8_quant_weights(elem, (int)code, w->data_ptr(), E, N, K, q, qs, qt, qts, s) == MOE_OK);
+  if (!c.plain || elem < 0) return not_plain();
+  return made(f_fp8_quant_weights(elem, (int)code, w->data_ptr(), E, N, K, q, qs, qt, qts, s));
 }
 
 // x, x_scale, w, w_scale, expert_ids, num_tokens_post_padded, block_m, out
@@ -209,19 +220,19 @@ PyObject* fp8_linear(PyObject* const* a) {
   const at::Tensor* xs = c.tensor(a[1]);
   const at::Tensor* w = c.tensor(a[2]);
   const at::Tensor* out = c.tensor(a[7]);
-  if (!c.plain || x->dim() != 2 || w->dim() != 3) return done(false);
+  if (!c.plain || x->dim() != 2 || w->dim() != 3) return not_plain();
   for (int i = 0; i < 4; ++i) c.outside_autograd(c.tensor(a[i]));
   const int64_t M = x->size(0), K = x->size(1), E = w->size(0), N = w->size(1);
   const int code = scale_of(xs->scalar_type()), elem = elem_of(out->scalar_type());
-  if (code < 0 || elem < 0 || elem > MOE_ELEM_F16) return done(false);
+  if (code < 0 || elem < 0 || elem > MOE_ELEM_F16) return not_plain();
   const int64_t block_m = c.integer(a[6], 0, kMost);
   const void* ids = nullptr;
   const void* ntp = nullptr;
   if (a[4] == Py_None) {
-    if (a[5] != Py_None || block_m) return done(false);
+    if (a[5] != Py_None || block_m) return not_plain();
   } else {
     const at::Tensor* e = c.tensor(a[4]);
-    if (!c.plain || block_m < 1 || e->numel() < (M + block_m - 1) / block_m) return done(false);
+    if (!c.plain || block_m < 1 || e->numel() < (M + block_m - 1) / block_m) return not_plain();
     ids = c.data(a[4], at::kInt, {e->numel()});
     ntp = c.data(a[5], at::kInt, {1});
   }
@@ -231,9 +242,9 @@ PyObject* fp8_linear(PyObject* const* a) {
   const void* wsp = c.data(a[3], scale_type(code), {E, groups(N), groups(K)});
   void* op = c.data(a[7], out->scalar_type(), {M, N});
   void* s = c.stream();
-  if (!c.plain || E > kMost) return done(false);
-  return done(f_fp8_linear(elem, code, xp, xsp, wp, wsp, static_cast<const int32_t*>(ids),
-                           static_cast<const int32_t*>(ntp), op, M, K, N, (int)E, (int)block_m, s) == MOE_OK);
+  if (!c.plain || E > kMost) return not_plain();
+  return made(f_fp8_linear(elem, code, xp, xsp, wp, wsp, static_cast<const int32_t*>(ids),
+                           static_cast<const int32_t*>(ntp), op, M, K, N, (int)E, (int)block_m, s));
 }
 
 // dyt, dyt_scale, xt, xt_scale, num_experts, expert_ids, num_tokens_post_padded, block_m, out
@@ -243,20 +254,20 @@ PyObject* fp8_linear_dw(PyObject* const* a) {
   const at::Tensor* dys = c.tensor(a[1]);
   const at::Tensor* x = c.tensor(a[2]);
   const at::Tensor* out = c.tensor(a[8]);
-  if (!c.plain || dy->dim() != 2 || x->dim() != 2) return done(false);
+  if (!c.plain || dy->dim() != 2 || x->dim() != 2) return not_plain();
   for (int i = 0; i < 4; ++i) c.outside_autograd(c.tensor(a[i]));
   const int64_t N = dy->size(0), M = dy->size(1), K = x->size(0), E = c.integer(a[4], 1, kMost);
   const int code = scale_of(dys->scalar_type()), elem = elem_of(out->scalar_type());
-  if (code < 0 || elem < 0 || elem > MOE_ELEM_F16 || M % 128) return done(false);
+  if (code < 0 || elem < 0 || elem > MOE_ELEM_F16 || M % 128) return not_plain();
   const int64_t block_m = c.integer(a[7], 0, kMost);
   const void* ids = nullptr;
   const void* ntp = nullptr;
   int64_t blocks = 0;
   if (a[5] == Py_None) {
-    if (a[6] != Py_None || block_m) return done(false);
+    if (a[6] != Py_None || block_m) return not_plain();
   } else {
     const at::Tensor* e = c.tensor(a[5]);
-    if (!c.plain || block_m < 1) return done(false);
+    if (!c.plain || block_m < 1) return not_plain();
     blocks = e->numel();
     ids = c.data(a[5], at::kInt, {blocks});
     ntp = c.data(a[6], at::kInt, {1});
@@ -267,15 +278,16 @@ PyObject* fp8_linear_dw(PyObject* const* a) {
   const void* xsp = c.data(a[3], scale_type(code), {K, M / 128});
   void* op = c.data(a[8], out->scalar_type(), {E, N, K});
   void* s = c.stream();
-  if (!c.plain) return done(false);
-  return done(f_fp8_linear_dw(elem, code, dp, dsp, xp, xsp, static_cast<const int32_t*>(ids),
-                              static_cast<const int32_t*>(ntp), op, M, N, K, (int)E, (int)block_m, blocks, s) == MOE_OK);
+  if (!c.plain) return not_plain();
+  return made(f_fp8_linear_dw(elem, code, dp, dsp, xp, xsp, static_cast<const int32_t*>(ids),
+                              static_cast<const int32_t*>(ntp), op, M, N, K, (int)E, (int)block_m, blocks, s));
 }
 
-// The library's handle (as dlopen gave it), and torch's function for the current stream.
+// The library's handle (as dlopen gave it), torch's function for the current stream, and
+// one that raises the error of a status.
 PyObject* init(PyObject*, PyObject* args) {
-  PyObject *handle, *stream;
-  if (!PyArg_ParseTuple(args, "OO", &handle, &stream)) return nullptr;
+  PyObject *handle, *stream, *failed = nullptr;
+  if (!PyArg_ParseTuple(args, "OO|O", &handle, &stream, &failed)) return nullptr;
   void* h = PyLong_AsVoidPtr(handle);
   if (PyErr_Occurred()) return nullptr;
   auto get = [&](auto& f, const char* name) {
@@ -292,6 +304,8 @@ PyObject* init(PyObject*, PyObject* args) {
   }
   Py_INCREF(stream);
   Py_XSETREF(raw_stream, stream);
+  Py_XINCREF(failed);
+  Py_XSETREF(launch_failed, failed);
   Py_RETURN_NONE;
 }
 
