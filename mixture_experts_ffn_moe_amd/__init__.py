@@ -31,6 +31,7 @@ moe_workspace_layout, moe_ring_layout, moe_select_split and moe_select_block_m.
 import ctypes
 import importlib
 import os
+import warnings
 
 import torch
 
@@ -167,15 +168,23 @@ def lib():
 _fast = None
 
 
+class _NothingPlain:
+    """In place of the module where it is missing or was built for another torch."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _short_way(L):
     global _fast
-    if _fast is None:
-        if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_fast.so")):
-            raise RuntimeError(
-                "_fast.so is missing beside the library: build both with "
-                "`python -m mixture_experts_ffn_moe_amd.build`")
-        _fast = importlib.import_module("._fast", __name__)
-    _fast.init(L._handle, torch._C._cuda_getCurrentRawStream, _check)
+    try:
+        if _fast is None:
+            _fast = importlib.import_module("._fast", __name__)
+        _fast.init(L._handle, torch._C._cuda_getCurrentRawStream, _check)
+    except (ImportError, RuntimeError) as e:
+        _fast = _NothingPlain()
+        warnings.warn(f"calls go the longer way through Python, without module _fast: {e} (build it beside the "
+                      "library with `python -m mixture_experts_ffn_moe_amd.build`)", RuntimeWarning)
 
 
 class MoeTune(ctypes.Structure):

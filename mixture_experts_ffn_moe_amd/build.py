@@ -53,6 +53,7 @@ def _compile_binding():
     tmp = FAST + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DBUILT_FOR_TORCH="{torch.__version__}"',
            *(x for p in includes for x in ("-isystem", p)),
            os.path.join(CSRC, "binding.cpp"), "-L" + libs, "-lc10", "-ltorch_cpu", "-ltorch_python",
            "-o", tmp]

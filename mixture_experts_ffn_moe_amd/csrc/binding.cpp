@@ -10,9 +10,14 @@
 // refuses: the binding in Python then goes its own way, which finds and words the
 // error, or serves the less plain call.  A launch that fails raises at once, since
 // the same call made again might succeed and hide it.
+//
+// Torch's and the interpreter's internals are compiled in: beside others than those
+// it was built for (BUILT_FOR_TORCH, torch's version) the module refuses to load, and
+// the binding does without it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <dlfcn.h>
+#include <cstdio>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/core/Tensor.h>
@@ -321,6 +326,24 @@ PyMethodDef methods[] = {
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
+// Whether this interpreter and this torch are the ones built for; sets an error if not.
+bool built_for_these() {
+  int major = 0, minor = 0;
+  const bool python = sscanf(Py_GetVersion(), "%d.%d", &major, &minor) == 2 && major == PY_MAJOR_VERSION &&
+                      minor == PY_MINOR_VERSION;
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  PyObject* text = version ? PyObject_Str(version) : nullptr;
+  const bool ok = text && python && PyUnicode_CompareWithASCIIString(text, BUILT_FOR_TORCH) == 0;
+  if (text && !ok)
+    PyErr_Format(PyExc_ImportError, "built for torch %s and Python %d.%d, not torch %U and Python %d.%d",
+                 BUILT_FOR_TORCH, PY_MAJOR_VERSION, PY_MINOR_VERSION, text, major, minor);
+  Py_XDECREF(text);
+  Py_XDECREF(version);
+  Py_XDECREF(torch);
+  return ok;
+}
+
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fast() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__fast() { return built_for_these() ? PyModule_Create(&module) : nullptr; }
