@@ -702,14 +702,17 @@ int fused_moe_w4(int32_t format, int32_t elem, const void* x, const void* w1, co
  *       groups of the largest scores keep their experts;
  *   topk_ids: the top_k largest c among those, in descending order;
  *   topk_weights: scale * s of the chosen, with renormalize divided by the
- *       chosen ones' sum first.
+ *       chosen ones' sum first: for a softmax that is the softmax over the
+ *       chosen logits, and computed as such, so that it holds also where bias
+ *       or groups choose experts whose s is 0 in 64 bits beside the others'.
  * Equal scores go to the lower index.  Scores are computed and compared in 64
  * bits, so that the choice does not hang on an exponential's rounding in 32.
  * An expert whose logit is -inf or NaN, or whose bias is, is masked: it is
  * never chosen, and takes no part in a softmax where its logit is.  Where fewer
  * than top_k experts are left, the rest of topk_ids is -1 (which the planner
  * skips) and of topk_weights 0.  A logit of +inf counts as fp32's largest.
- * Chosen scores whose sum is 0 in 64 bits get weights 0.
+ * Sigmoids of the chosen whose sum is 0 in 64 bits (logits below -709) get
+ * weights 0, and no gradient.
  *   elem     MOE_ELEM_BF16, MOE_ELEM_F16 or MOE_ELEM_F32: logits (T, E).
  *   bias     (E) fp32, or NULL for none.  It takes part in the choice only and
  *            has no gradient.

@@ -102,7 +102,7 @@ def route_topk_backward_ref(logits, ids, d_weights, scoring, renormalize, scale)
             S = v.sum()
             if S == 0:
                 continue
-            g = (np.eye(len(at)) / S - np.outer(np.ones(len(at)), v) / S ** 2) @ g
+            g = (np.eye(len(at)) - np.outer(np.ones(len(at)), v / S)) @ g / S  # (S squared may be 0)
         ds = np.zeros(E)
         np.add.at(ds, e, g)
         if scoring == "sigmoid":
