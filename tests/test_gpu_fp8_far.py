@@ -1,0 +1,199 @@
+"""8-bit quantizers and linear layers at their limits: contractions of 2^22, and
+tensors whose offsets pass 32 bits.
+
+Products: all but some 300 columns are zeros, among them the first and the last and
+those around powers of two, so that the result is the exact one of those columns
+(whole values, scales powers of two), rounded once.  Quantizers: bit for bit the
+oracle's, at rows, columns and blocks from all over the tensor."""
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_ffn_moe_amd as moe
+from oracle import fp8
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ("f32", "e8m0")
+F8, I32 = torch.float8_e4m3fn, torch.int32
+LIMIT = 1 << 22
+
+
+@pytest.fixture(scope="module", autouse=True)
+def give_memory_back():
+    yield
+    torch.cuda.empty_cache()
+
+
+def generator(n):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    return g
+
+
+def places(K, g):
+    """Some 300 columns of K, sorted."""
+    p = [torch.randint(0, K, (260,), generator=g, device="cuda").cpu(), torch.tensor([0, 1, 15, 16, 127, 128, K - 1, K - 16, K - 17])]
+    p += [torch.tensor([(1 << n) - 1, 1 << n]) for n in range(8, K.bit_length() - 1)]
+    return torch.cat(p).unique().cuda()
+
+
+def operand(rows, K, at, scale_rows, kind, g):
+    """(codes (rows, K), scales (scale_rows, ceil(K / 128)), their values): whole values at the columns `at`."""
+    v = torch.randint(-2, 3, (rows, len(at)), generator=g, device="cuda").float()
+    q = torch.zeros(rows, K, dtype=torch.uint8, device="cuda")
+    q[:, at] = v.to(F8).view(torch.uint8)
+    e = torch.randint(-1, 2, (scale_rows, -(-K // 128)), generator=g, device="cuda")
+    s = torch.exp2(e.float()) if kind == "f32" else (e + 127).to(torch.uint8)
+    f = torch.exp2(e.double())[:, at // 128]
+    return q.view(F8), s, v.double(), f
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,N", [(3, 40), (20, 4100), (200, 520), (1900, 2100), (4500, 4600)])
+def test_long_contraction(M, N, kind):
+    for K in (LIMIT, LIMIT - 16):
+        g = generator(M + N)
+        at = places(K, g)
+        x, xs, xv, xf = operand(M, K, at, M, kind, g)
+        w, ws, wv, wf = operand(N, K, at, -(-N // 128), kind, g)
+        out = moe.moe_fp8_linear(x, xs, w[None], ws[None])
+        want = (xv * xf) @ (wv * wf.repeat_interleave(128, 0)[:N]).T.contiguous()
+        assert torch.equal(out, want.to(out.dtype))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("N,K", [(40, 72), (500, 520), (4500, 4600)])
+def test_gradient_over_many_rows(N, K, kind):
+    g = generator(N)
+    at = places(LIMIT, g)
+    dy, ds, dv, df = operand(N, LIMIT, at, N, kind, g)
+    x, xs, xv, xf = operand(K, LIMIT, at, K, kind, g)
+    out = moe.moe_fp8_linear_dw(dy, ds, x, xs)
+    want = (dv * df) @ (xv * xf).T.contiguous()
+    assert torch.equal(out[0], want.to(out.dtype))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("N,K,bm", [(40, 72, 128), (700, 800, 256), (2300, 2304, 256)])
+def test_gradient_over_a_long_plan(N, K, bm, kind):
+    g = generator(N)
+    at = places(LIMIT, g)
+    n, E = LIMIT // bm, 3
+    ids = torch.full((n,), 2, dtype=I32, device="cuda")  # expert 1 has no rows, and 2 most of them
+    ids[:5] = -1
+    ids[5:77] = 0
+    ntp = torch.tensor([LIMIT - bm], dtype=I32, device="cuda")
+    dy, ds, dv, df = operand(N, LIMIT, at, N, kind, g)
+    x, xs, xv, xf = operand(K, LIMIT, at, K, kind, g)
+    out = moe.moe_fp8_linear_dw(dy, ds, x, xs, E, ids, ntp, bm)
+    of = ids[at // bm].clone()
+    of[at >= LIMIT - bm] = -1
+    for e in range(E):
+        mine = (of == e).double()
+        want = (dv * df * mine) @ (xv * xf).T.contiguous()
+        assert torch.equal(out[e], want.to(out.dtype))
+        assert e == 1 or bool(want.any())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_rows_past_4_gib(kind):
+    M, K, N, bm, E = 300_000, 16400, 24, 128, 2
+    g = generator(1)
+    at = places(K, g)
+    x, xs, xv, xf = operand(M, K, at, M, kind, g)
+    w, ws, wv, wf = operand(E * N, K, at, E, kind, g)
+    w, ws = w.reshape(E, N, K), ws.reshape(E, 1, -1)
+    want = torch.stack([(xv * xf) @ (wv[e * N:e * N + N] * wf[e]).T.contiguous() for e in range(E)])
+    out = moe.moe_fp8_linear(x, xs, w[:1], ws[:1])
+    assert torch.equal(out, want[0].to(out.dtype))
+    # and block by block of a plan, all rows but the last 1000 in use
+    ids = torch.randint(0, E, (-(-M // bm),), generator=g, device="cuda").to(I32)
+    ntp = torch.tensor([M - 1000], dtype=I32, device="cuda")
+    out = torch.full((M, N), 1234.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_fp8_linear(x, xs, w, ws, ids, ntp, bm, out=out)
+    of = ids.repeat_interleave(bm)[:M].long()
+    chosen = want.gather(0, of[None, :, None].expand(1, M, N))[0].to(out.dtype)
+    assert torch.equal(out[:M - 1000], chosen[:M - 1000]) and bool((out[M - 1000:] == 1234.0).all())
+
+
+@pytest.mark.parametrize("bm", [16, 32, 64, 128, 256])
+def test_weights_past_4_gib(bm):
+    E, N, K = 300, 1000, 16400
+    g = generator(bm)
+    at = places(K, g)
+    x, xs, xv, xf = operand(7 * bm, K, at, 7 * bm, "e8m0", g)
+    w, ws, wv, wf = operand(E * N, K, at, E * 8, "e8m0", g)
+    ids = torch.tensor([0, 1, 150, 262, 263, 298, 299], dtype=I32, device="cuda")
+    ntp = torch.tensor([7 * bm], dtype=I32, device="cuda")
+    out = moe.moe_fp8_linear(x, xs, w.reshape(E, N, K), ws.reshape(E, 8, -1), ids, ntp, bm)
+    for b, e in enumerate(ids.tolist()):
+        f = wf[e * 8:e * 8 + 8].repeat_interleave(128, 0)[:N]
+        rows = slice(b * bm, b * bm + bm)
+        want = (xv[rows] * xf[rows]) @ (wv[e * N:e * N + N] * f).T.contiguous()
+        assert torch.equal(out[rows], want.to(out.dtype))
+
+
+def same(q, s, ref):
+    return np.array_equal(q.view(torch.uint8).cpu().numpy(), ref[0]) and np.array_equal(s.cpu().numpy(), ref[1])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,K,elem", [(300, 16400, torch.bfloat16), (299, 16400, torch.float32), (270_000, 16400, torch.float16)])
+def test_quantized_rows(M, K, elem, kind):
+    # over 32,768 groups of 128, where a thread takes four, the last ones not whole; over 2^32 values
+    g = generator(M)
+    if elem is torch.float16:  # any finite bits
+        x = torch.randint(0, 0x7C00, (M, K), generator=g, dtype=torch.int16, device="cuda").view(elem)
+        x[:, 1::2].neg_()
+    else:
+        x = torch.randn(M, K, generator=g, dtype=elem, device="cuda")
+    q, s, _, _ = moe.moe_fp8_quant(x, kind)
+    at = torch.tensor([0, 1, 15, 16, 17, M // 3, M // 2, M - 2, M - 1], device="cuda")
+    assert same(q[at], s[at], fp8.quant_rows(x[at].float().cpu().numpy(), kind))
+    if M < 1000:
+        f = x.float().cpu()
+        a = torch.nn.functional.pad(f, (0, -K % 128)).reshape(M, -1, 128)
+        amax = a.abs().amax(2).clamp(min=1e-30)
+        if kind == "f32":
+            held = amax * torch.tensor(1.0 / 448.0)
+            factor = 1.0 / held
+        else:
+            m, e = torch.frexp(amax)  # amax = m 2^e, 448 = 0.875 2^9
+            e = e - 9 + (m > 0.875).int()
+            held, factor = (e + 127).to(torch.uint8), torch.ldexp(torch.tensor(1.0), -e)
+        assert torch.equal(s.cpu(), held)
+        codes = (a * factor[..., None]).reshape(M, -1)[:, :K].to(F8)
+        assert torch.equal(q.cpu().view(torch.uint8), codes.view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_quantized_columns_past_4_gib(kind):
+    M, K = 300_001, 16400
+    g = generator(4)
+    x = torch.randn(M, K, generator=g, dtype=torch.bfloat16, device="cuda")
+    for rows in (False, True):
+        q, s, qt, st = moe.moe_fp8_quant(x, kind, rows=rows, columns=True)
+        for m0, m1 in ((0, 128), (261_888, 262_144), (299_904, M)):  # the last 128 begin at 299,904
+            cut = x[m0:m1, ::1171].float().cpu().numpy()
+            ref = fp8.quant_columns(np.ascontiguousarray(cut), kind)
+            assert same(qt[::1171, m0:m0 + ref[0].shape[1]], st[::1171, m0 // 128:m0 // 128 + ref[1].shape[1]], ref)
+        assert qt.shape == (K, 300_032) and not qt.view(torch.uint8)[:, M:].any()
+        if rows:
+            at = torch.tensor([0, 262_143, M - 1], device="cuda")
+            assert same(q[at], s[at], fp8.quant_rows(x[at].float().cpu().numpy(), kind))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_quantized_weights_past_4_gib(kind):
+    E, N, K = 300, 1008, 16400
+    g = generator(5)
+    w = torch.randn(E, N, K, generator=g, dtype=torch.bfloat16, device="cuda")
+    q, s, qt, st = moe.moe_fp8_quant_weights(w, kind, transposed=True)
+    for e in (0, 129, 261, 299):
+        for n0, k0 in ((0, 0), (896, 16384), (512, 8192)):
+            n, k = slice(n0, min(n0 + 128, N)), slice(k0, min(k0 + 128, K))
+            ref = fp8.quant_blocks(w[e, n, k].float().cpu().numpy(), kind)
+            assert same(q[e, n, k], s[e, n0 // 128:n0 // 128 + 1, k0 // 128:k0 // 128 + 1], ref)
+            assert same(qt[e, k, n], st[e, k0 // 128:k0 // 128 + 1, n0 // 128:n0 // 128 + 1], (ref[0].T, ref[1].T))
