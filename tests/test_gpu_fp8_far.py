@@ -197,3 +197,21 @@ def test_quantized_weights_past_4_gib(kind):
             ref = fp8.quant_blocks(w[e, n, k].float().cpu().numpy(), kind)
             assert same(q[e, n, k], s[e, n0 // 128:n0 // 128 + 1, k0 // 128:k0 // 128 + 1], ref)
             assert same(qt[e, k, n], st[e, k0 // 128:k0 // 128 + 1, n0 // 128:n0 // 128 + 1], (ref[0].T, ref[1].T))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_more_experts_than_a_tile_list_can_name(kind):
+    # 600,000 experts: the list of joined blocks has 19 bits for one, so that each block is a tile
+    E, N, K, bm, n = 600_000, 16, 32, 128, 547
+    g = generator(6)
+    ids = torch.randint(0, E, (n,), generator=g, device="cuda").to(I32)
+    ids[3], ids[4], ids[5], ids[6] = E - 1, E, -1, 524_287
+    x, xs, xv, xf = operand(n * bm, K, torch.arange(K, device="cuda"), n * bm, kind, g)
+    w, ws, wv, wf = operand(E * N, K, torch.arange(K, device="cuda"), E, kind, g)
+    ntp = torch.tensor([n * bm], dtype=I32, device="cuda")
+    out = moe.moe_fp8_linear(x, xs, w.reshape(E, N, K), ws.reshape(E, 1, 1), ids, ntp, bm)
+    here = ((ids >= 0) & (ids < E)).double()[:, None, None]
+    at = ids.clamp(0, E - 1).long()
+    mine = (wv * wf.repeat_interleave(N, 0)).reshape(E, N, K)[at] * here
+    want = torch.bmm((xv * xf).reshape(n, bm, K), mine.transpose(1, 2).contiguous())
+    assert torch.equal(out, want.reshape(n * bm, N).to(out.dtype))

@@ -65,7 +65,7 @@ DW_PLAN = [
     (20, 3, 128, 300, 400, "tile<64, 64, 16, 2, 3>"), (20, 3, 128, 500, 1200, "tile<64, 128, 32, 2, 3>"),
     (20, 3, 128, 900, 1200, "tile<128, 128, 64, 2, 2>"), (20, 3, 128, 1500, 1500, "tile<128, 128, 32, 1, 2>"),
     (40, 4, 128, 2304, 2304, "stay"), (40, 4, 128, 2300, 2305, "stay"), (15, 3, 256, 2500, 2504, "stay"),
-    (30, 40, 128, 700, 1000, "stay"),
+    (30, 40, 128, 700, 1000, "stay"), (300, 1024, 128, 32, 48, "stay"),
 ]
 
 
