@@ -159,7 +159,7 @@ k_quant_rows(QuantArgs a, uint32_t G, uint32_t total) {
 // BLOCK: one scale for the tile (weights; blockIdx.z the expert), q and, with COLS,
 // its transpose.  Else ROWS and COLS with scales of their own.
 // x is read once for both forms.  Bound by HBM: weights 8 x 4096 x 4096 fp32 in 149
-// us, 5.4 TB/s; rows and columns of 8192 x 4096 bf16 in 31, 4.3 TB/s, where the
+// us, 5.4 TB/s (a plain conversion of these bytes, two read for one written: 137); rows and columns of 8192 x 4096 bf16 in 31, 4.3 TB/s, where the
 // conversions of both forms take turns with the loads.
 //
 // In LDS a column is 128 bytes and every access 8 or 16.  A wave writes 8 bytes of 16
