@@ -900,7 +900,7 @@ def moe_route_topk(logits, top_k, bias=None, scoring="softmax", n_group=1, topk_
     ``n_group`` groups whose ``group_top`` (1 or 2) largest add up to most.
     Weights are the chosen ones' scores without the bias, divided by their sum
     with ``renormalize`` (a softmax over the chosen logits, or the sigmoids over
-    their sum), times ``scale``.  A logit of -inf or NaN masks an
+    their sum), times ``scale`` (as fp32 holds it).  A logit of -inf or NaN masks an
     expert; where fewer than top_k are left, ids are -1 and weights 0.  The
     planner (moe_align) takes the ids as they are.  ``out`` may pass the two
     preallocated.  moe_route_topk_backward is its gradient: with gradients
