@@ -181,7 +181,7 @@ def _short_way(L):
         if _fast is None:
             _fast = importlib.import_module("._fast", __name__)
         _fast.init(L._handle, torch._C._cuda_getCurrentRawStream, _check)
-    except (ImportError, RuntimeError) as e:
+    except (ImportError, RuntimeError, TypeError) as e:  # TypeError: a module of an older build
         _fast = _NothingPlain()
         warnings.warn(f"calls go the longer way through Python, without module _fast: {e} (build it beside the "
                       "library with `python -m mixture_experts_ffn_moe_amd.build`)", RuntimeWarning)

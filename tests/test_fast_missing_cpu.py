@@ -31,14 +31,15 @@ CALLS = {
 }
 
 
-@pytest.fixture(params=["missing", "unloadable", "another library"])
+@pytest.fixture(params=["missing", "unloadable", "another library", "an older build"])
 def without(request, monkeypatch):
     moe.lib()
-    if request.param == "another library":
+    if request.param in ("another library", "an older build"):
         class Module:
             @staticmethod
             def init(*a):
-                raise RuntimeError("the library lacks an entry point")
+                raise RuntimeError("the library lacks an entry point") if request.param == "another library" else \
+                    TypeError("function takes exactly 2 arguments (3 given)")
         found = lambda *a: Module  # noqa: E731
     else:
         kind = ModuleNotFoundError if request.param == "missing" else ImportError
